@@ -22,10 +22,13 @@ __all__ = [
     "wr_gemv_ternary_batched_workspace_bytes", "wr_gemv_ternary_batched", "wr_selftest_wait_timeout",
     "wr_quantize_pack", "wr_quantize_trellis", "WR_FMT_T2", "WR_FMT_T8", "wr_quantize_trellis8", "WR_SCALES_I8", "wr_scales_bytes",
     "wr_gemv_batched_plan", "WrGemvGroupItem", "wr_gemv_grouped_workspace_bytes", "wr_gemv_grouped",
+    "WR_F32", "WR_BF16", "WR_F16", "WR_I8", "wr_quantize_rows", "wr_gemm_i8_workspace_bytes", "wr_gemm_i8",
+    "WrResidualNormArgs", "wr_residual_norm",
 ]
 
 WR_FMT_TERNARY, WR_FMT_Q2, WR_FMT_Q3, WR_FMT_T2, WR_FMT_T8 = 1, 2, 3, 4, 5
 WR_SCALES_I8 = 0x100   # OR'd into a format code: int8 block scales (the scale record of include/wr.h)
+WR_F32, WR_BF16, WR_F16, WR_I8 = 0, 1, 2, 3   # element types of the 8-bit token path
 WR_GEMV_NOALLOC_SCRATCH_BYTES = 4 << 20   # mirrors the macro in include/wr.h
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwr.so")
 
@@ -59,6 +62,15 @@ class WrGemvGroupItem(ctypes.Structure):
 
 _GITEMS = ctypes.POINTER(WrGemvGroupItem)
 
+class WrResidualNormArgs(ctypes.Structure):
+    """Mirror of the C struct wr_residual_norm_args."""
+    _fields_ = [(n, _c_i64) for n in ("M", "D")] + \
+        [(n, _vp) for n in ("block", "residual", "gate", "post_weight", "norm_weight", "residual_out", "y", "y_scale")] + \
+        [(n, _c_i64) for n in ("ld_block", "ld_residual", "ld_gate", "ld_residual_out", "ld_y")] + \
+        [(n, ctypes.c_int32) for n in ("block_type", "residual_type", "gate_type", "weight_type", "y_type", "post_norm")] + \
+        [(n, ctypes.c_float) for n in ("eps", "residual_scale", "weight_offset")] + [("reserved", ctypes.c_int32)]
+
+
 _SIGNATURES = {
     "wr_abi_version": (_c_int, []),
     "wr_status_string": (ctypes.c_char_p, [_c_int]),
@@ -88,6 +100,11 @@ _SIGNATURES = {
     "wr_gemv_noalloc": (_c_int, [_c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp]),
     "wr_gemv_ternary_batched_workspace_bytes": (_c_size, [_c_i64, ctypes.c_int32, _TPROBLEMS]),
     "wr_gemv_ternary_batched": (_c_int, [_c_i64, ctypes.c_int32, _TPROBLEMS, _vp, _c_size, _vp]),
+    "wr_quantize_rows": (_c_int, [_c_int, _c_i64, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _c_i64, _vp, _vp]),
+    "wr_gemm_i8_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "wr_gemm_i8": (_c_int, [_c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _vp, _vp, _c_int, _vp, _c_i64, _vp,
+                            _c_size, _vp]),
+    "wr_residual_norm": (_c_int, [ctypes.POINTER(WrResidualNormArgs), _vp]),
 }
 
 
@@ -351,6 +368,55 @@ def wr_quantize_pack(bits: int, N: int, K: int, w, packed, scales, stream=None) 
     the int8 scale record (wr_scales_bytes bytes)."""
     _check("wr_quantize_pack", _lib.wr_quantize_pack(bits, N, K, _ptr(w), _ptr(packed), _ptr(scales),
                                                      _stream(stream)))
+
+
+def _dptr(t) -> int | None:
+    """Address of a device operand of the 8-bit token path: a tensor has to be on the current CUDA
+    device (the library launches there), an int is taken as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor, got one on the host")
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on cuda:{t.get_device()}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def wr_quantize_rows(type: int, M: int, K: int, x, ldx: int, q, ldq: int, scale, gate=None, ldg: int = 0,
+                     stream=None) -> None:
+    """Rows of x (or of silu(gate) * x) -> int8 codes q and one fp32 scale per row (device)."""
+    _check("wr_quantize_rows", _lib.wr_quantize_rows(type, M, K, _dptr(x), ldx, _dptr(gate), ldg, _dptr(q), ldq,
+                                                     _dptr(scale), _stream(stream)))
+
+
+def wr_gemm_i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _lib.wr_gemm_i8_workspace_bytes(M, N, K)
+
+
+def wr_gemm_i8(M: int, N: int, K: int, x, ldx: int, x_scale, w, ldw: int, w_scale, y_type: int, y, ldy: int, workspace,
+               workspace_bytes: int, bias=None, stream=None) -> None:
+    """y = (x w^T) * x_scale[:, None] * w_scale (+ bias) from int8 tokens and int8 output channels."""
+    _check("wr_gemm_i8", _lib.wr_gemm_i8(M, N, K, _dptr(x), ldx, _dptr(x_scale), _dptr(w), ldw, _dptr(w_scale),
+                                         _dptr(bias), y_type, _dptr(y), ldy, _dptr(workspace), workspace_bytes,
+                                         _stream(stream)))
+
+
+def wr_residual_norm(M: int, D: int, *, block=None, ld_block: int = 0, block_type: int = WR_F32, residual=None,
+                     ld_residual: int = 0, residual_out=None, ld_residual_out: int = 0, residual_type: int = WR_F32,
+                     gate=None, ld_gate: int = 0, gate_type: int = WR_F32, post_weight=None, norm_weight=None,
+                     weight_type: int = WR_F32, weight_offset: float = 0.0, post_norm: bool | None = None, y=None,
+                     ld_y: int = 0, y_type: int = WR_F32, y_scale=None, residual_scale: float = 1.0, eps: float = 1e-6,
+                     stream=None) -> None:
+    """h' = residual_scale * residual + gate * post(block) and y = norm(h'), in one pass (wr_residual_norm
+    of include/wr.h). post_norm: whether the block's output is normed first; by default, whether
+    post_weight is given."""
+    a = WrResidualNormArgs(M, D, _dptr(block), _dptr(residual), _dptr(gate), _dptr(post_weight), _dptr(norm_weight),
+                           _dptr(residual_out), _dptr(y), _dptr(y_scale), ld_block, ld_residual, ld_gate, ld_residual_out,
+                           ld_y, block_type, residual_type, gate_type, weight_type, y_type,
+                           post_weight is not None if post_norm is None else post_norm, eps, residual_scale,
+                           weight_offset, 0)
+    _check("wr_residual_norm", _lib.wr_residual_norm(a, _stream(stream)))
 
 
 def wr_selftest_wait_timeout(stream=None) -> None:

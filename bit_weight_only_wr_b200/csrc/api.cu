@@ -6,9 +6,11 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
+#include "i8_kernels.cuh"
 #include "tc_kernels.cuh"
 #include "wr.h"
 #include "wr_internal.h"
@@ -656,6 +658,95 @@ wr_status wr_quantize_pack(int bits, int64_t N, int64_t K, const float* w, void*
                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? WR_OK
              : WR_ERR_CUDA;
+}
+
+// A row-major operand: `rows` rows of `cols` elements, ld apart, whose last byte has an address.
+static bool float_type(int t) { return t == WR_F32 || t == WR_BF16 || t == WR_F16; }
+static bool stride_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && ld <= kMaxDim * 4 && (double)rows * (double)ld <= 1.0e17;
+}
+
+wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_t ldx, const void* gate, int64_t ldg,
+                           int8_t* q, int64_t ldq, float* scale, void* stream) {
+  if (!float_type(type)) return WR_ERR_UNSUPPORTED;
+  if (check_dims(M, 1, K) != WR_OK) return WR_ERR_INVALID_ARG;
+  if (!stride_ok(M, K, ldx) || !stride_ok(M, K, ldq) || (gate && !stride_ok(M, K, ldg))) return WR_ERR_INVALID_ARG;
+  if (!aligned16(x) || (gate && !aligned16(gate)) || !aligned16(q) || !aligned16(scale)) return WR_ERR_INVALID_ARG;
+  wr::QuantRowsArgs a{};
+  a.x = static_cast<const uint8_t*>(x);
+  a.gate = static_cast<const uint8_t*>(gate);
+  a.q = q;
+  a.scale = scale;
+  a.ldx = ldx;
+  a.ldg = ldg;
+  a.ldq = ldq;
+  a.M = M;
+  a.K = (int)K;
+  a.type = type;
+  return wr::launch_quantize_rows(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WR_OK : WR_ERR_CUDA;
+}
+
+size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (check_dims(M, N, K) != WR_OK || K > wr::kMaxI8K) return 0;
+  return 0;
+}
+
+wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
+                     const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,
+                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!float_type(y_type)) return WR_ERR_UNSUPPORTED;
+  if (check_dims(M, N, K) != WR_OK) return WR_ERR_INVALID_ARG;
+  if (K > wr::kMaxI8K) return WR_ERR_UNSUPPORTED;
+  if (!stride_ok(M, K, ldx) || !stride_ok(N, K, ldw) || !stride_ok(M, N, ldy) || ldx % 16 != 0 || ldw % 16 != 0)
+    return WR_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || (bias && !aligned16(bias)) ||
+      !aligned16(y))
+    return WR_ERR_INVALID_ARG;
+  const size_t need = wr_gemm_i8_workspace_bytes(M, N, K);
+  if (need > 0 && (!aligned16(workspace) || workspace_bytes < need)) return WR_ERR_INVALID_ARG;
+  wr::GemmI8Args a{};
+  a.x = x;
+  a.w = w;
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.y = y;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.y_type = y_type;
+  return wr::launch_gemv_i8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WR_OK : WR_ERR_CUDA;
+}
+
+wr_status wr_residual_norm(const wr_residual_norm_args* p, void* stream) {
+  if (!p) return WR_ERR_INVALID_ARG;
+  const wr_residual_norm_args& a = *p;
+  if ((a.block && !float_type(a.block_type)) || (a.residual && !float_type(a.residual_type)) ||
+      (a.residual_out && !float_type(a.residual_type)) || (a.gate && !float_type(a.gate_type)) ||
+      ((a.post_weight || a.norm_weight) && !float_type(a.weight_type)) ||
+      (a.y && !float_type(a.y_type) && a.y_type != WR_I8))
+    return WR_ERR_UNSUPPORTED;
+  if (check_dims(a.M, 1, a.D) != WR_OK || a.reserved != 0 || (a.post_norm != 0 && a.post_norm != 1)) return WR_ERR_INVALID_ARG;
+  if (a.D > wr::kMaxNormDim) return WR_ERR_UNSUPPORTED;
+  if ((!a.block && !a.residual) || (!a.residual_out && !a.y)) return WR_ERR_INVALID_ARG;
+  if (!a.block && (a.gate || a.post_norm)) return WR_ERR_INVALID_ARG;
+  if (a.post_weight && !a.post_norm) return WR_ERR_INVALID_ARG;
+  if (a.norm_weight && !a.y) return WR_ERR_INVALID_ARG;
+  if (a.y ? (a.y_type == WR_I8) != (a.y_scale != nullptr) : a.y_scale != nullptr) return WR_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.f) || !std::isfinite(a.eps) || !std::isfinite(a.residual_scale) || !std::isfinite(a.weight_offset))
+    return WR_ERR_INVALID_ARG;
+  const void* ptrs[] = {a.block, a.residual, a.gate, a.post_weight, a.norm_weight, a.residual_out, a.y, a.y_scale};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return WR_ERR_INVALID_ARG;
+  if ((a.block && !stride_ok(a.M, a.D, a.ld_block)) || (a.residual && !stride_ok(a.M, a.D, a.ld_residual)) ||
+      (a.gate && a.ld_gate != 0 && !stride_ok(a.M, a.D, a.ld_gate)) ||
+      (a.residual_out && !stride_ok(a.M, a.D, a.ld_residual_out)) || (a.y && !stride_ok(a.M, a.D, a.ld_y)))
+    return WR_ERR_INVALID_ARG;
+  if (a.residual_out && a.residual_out == a.residual && a.ld_residual_out != a.ld_residual) return WR_ERR_INVALID_ARG;
+  return wr::launch_residual_norm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WR_OK : WR_ERR_CUDA;
 }
 
 wr_status wr_selftest_wait_timeout(void* stream) {

@@ -327,6 +327,74 @@ size_t wr_gemv_ternary_batched_workspace_bytes(int64_t M, int32_t count,
 wr_status wr_gemv_ternary_batched(int64_t M, int32_t count, const wr_gemv_ternary_problem* problems_host,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The 8-bit token path: linears that stay at 8 bits (a scale for each token and each output
+ * channel) and what stands between two linears. The 2.6-bit containers keep some tensors at higher
+ * precision ("Qwen3-4B-Wringer-Q2.6", "Honest caveats"), and the calls above write fp32 outputs that
+ * have to become the bf16 activations of the next call: wr_residual_norm is that step, and writes
+ * either those or the 8-bit tokens of wr_gemm_i8. No counterpart in the pages.
+ *
+ * Element types of these calls. Strides (ld*) are in elements, from one row to the next; a row's
+ * elements are contiguous. Nothing between two rows is read or written, nor anything behind the last
+ * element of the last row. Base pointers are 16-byte aligned as everywhere; rows that all start on 16
+ * bytes are moved in 16-byte pieces, others element by element (slower). Outputs must not overlap
+ * inputs except where stated. */
+enum { WR_F32 = 0, WR_BF16 = 1, WR_F16 = 2, WR_I8 = 3 };
+
+/* Row quantizer (device): for each of M rows of K values v = x[m,k], or v = silu(gate[m,k]) * x[m,k]
+ * in fp32 where gate is not null (the input of an MLP's down projection from its gate and up products,
+ * which may be two halves of one buffer), with silu(g) = g / (1 + exp(-g)):
+ *     scale[m] = A / 127,  A = max_k |v|        (fp32)
+ *     q[m,k]   = the integer nearest to 127 v / A, a tie to the even one
+ * so that v is about q * scale. The choice of q is exact for the fp32 value v (decided on the exact
+ * quotient). A row of zeros has scale 0 and codes 0; a row with an infinity or a NaN has scale NaN
+ * and codes 0, so that everything computed from it is NaN. Rows may be tokens (scale = wr_gemm_i8's
+ * x_scale) or the output channels of a weight matrix (w_scale). x and gate are of `type` WR_F32,
+ * WR_BF16 or WR_F16 (ldx, ldg >= K); q int8 (ldq >= K; a multiple of 16 is what wr_gemm_i8 takes);
+ * scale fp32 [M]. M, K >= 1. */
+wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_t ldx, const void* gate, int64_t ldg,
+                           int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* Int8 product, any M >= 1: y[m,n] = (sum_k x[m,k] w[n,k]) * x_scale[m] * w_scale[n] (+ bias[n]).
+ * x int8 [M, ldx] tokens, w int8 [N, ldw] output channels (K-major, ldx and ldw multiples of 16 and
+ * >= K, any K up to 131071 inside; larger K is WR_ERR_UNSUPPORTED: an int32 sum could overflow),
+ * x_scale fp32 [M], w_scale fp32 [N], bias fp32 [N] or null; y of y_type WR_F32, WR_BF16 or WR_F16
+ * (ldy >= N). The sums are exact integers; the fp32 conversion, the two products (x_scale first) and
+ * the bias round once each, then the type of y does: the result is the same bits on every run and for
+ * every M. The workspace rules are those of the other calls (a size of 0 means that none is needed;
+ * the pointer may then be null). */
+size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
+                     const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,
+                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Residual and norm around a block (fields read on the host during the call):
+ *     h'   = residual_scale * residual + gate * post(block)
+ *     post(b) = b, or with post_norm b / sqrt(mean(b^2) + eps) * (post_weight + weight_offset)
+ *     y    = h' / sqrt(mean(h'^2) + eps) * (norm_weight + weight_offset)
+ * over rows of D elements, in fp32 with one rounding to each output's type; the second norm takes h'
+ * before it is rounded to residual_out. y of y_type WR_F32, WR_BF16 or WR_F16, or WR_I8: then y holds
+ * wr_quantize_rows' codes of the fp32 values and y_scale [M] their scales. Null pointers: no block
+ * (h' = residual_scale * residual; gate null, post_norm 0), no residual (h' = gate * post(block)), no
+ * gate (1), no post_weight or norm_weight (1, without the offset), residual_out or y not written; block
+ * or residual, and residual_out or y, have to be there. residual_out may be residual (with the same
+ * stride); other outputs overlap no input. ld_gate = 0: one gate vector for all rows. Types: block,
+ * residual (and residual_out), gate and weights each WR_F32, WR_BF16 or WR_F16 (0 where unused).
+ * 1 <= D <= 32768 (larger D: WR_ERR_UNSUPPORTED); eps >= 0, all three floats finite. A row of zeros
+ * needs eps > 0 to stay zero (0 / 0 otherwise); squares are summed in fp32. */
+typedef struct {
+  int64_t M, D;
+  const void *block, *residual, *gate;
+  const void *post_weight, *norm_weight;   /* [D], of weight_type */
+  void *residual_out, *y;
+  float* y_scale;                          /* fp32 [M] with y_type WR_I8, else null */
+  int64_t ld_block, ld_residual, ld_gate, ld_residual_out, ld_y;
+  int32_t block_type, residual_type, gate_type, weight_type, y_type;
+  int32_t post_norm;                       /* 0 or 1 */
+  float eps, residual_scale, weight_offset;
+  int32_t reserved;                        /* must be 0 */
+} wr_residual_norm_args;
+wr_status wr_residual_norm(const wr_residual_norm_args* args_host, void* stream);
+
 /* Reads and clears the device error word that bounded waits set when they give up
  * (synchronizes the stream). WR_OK when no wait timed out since the last call. */
 wr_status wr_get_device_error(void* stream);

@@ -251,6 +251,85 @@ __device__ __forceinline__ void mma8_i8_commit_elect(uint32_t d_tmem, uint32_t a
       : "memory");
 }
 
+// kind::i8 instruction descriptor: int32 accumulator, A and B signed int8, K-major.
+__host__ __device__ constexpr uint32_t idesc_i8s(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// The 4 K steps of 32 of one 128-byte stage, both operands in shared memory, and the commit that
+// frees the stage: one election for the five instructions (see mma8_i8_commit_elect). The first step
+// overwrites D unless `accumulate`. PAIR: the CTA pair's MMA (256 rows, each CTA holds 128 of A and
+// half of B at the same shared-memory addresses); the commit arrives in both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void mma4_i8_ss_commit_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                        uint32_t accumulate, uint64_t* bar) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n .reg .pred e, p;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::2.kind::i8 [%0], %5, %6, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::2.kind::i8 [%0], %7, %8, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::2.kind::i8 [%0], %9, %10, %3, 1;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12;\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "l"(a_desc + 2), "l"(b_desc + 2), "l"(a_desc + 4), "l"(b_desc + 4),
+        "l"(a_desc + 6), "l"(b_desc + 6), "r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred e, p;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %5, %6, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %7, %8, %3, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::i8 [%0], %9, %10, %3, 1;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "l"(a_desc + 2), "l"(b_desc + 2), "l"(a_desc + 4), "l"(b_desc + 4),
+        "l"(a_desc + 6), "l"(b_desc + 6), "r"(smem_u32(bar))
+        : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- CTA pairs (cta_group::2)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Address of this CTA's shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// tma_load_2d into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
 // Shared-memory descriptor of a K-major operand tile stored with the 128-byte swizzle
 // (rows of 128 bytes, 8-row groups 1024 bytes apart).
 __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {

@@ -1,5 +1,6 @@
 // Launch interface of the tcgen05 GEMV/GEMM kernels (internal to libwr).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -137,6 +138,9 @@ __host__ __device__ inline bool decode_one_acc(int M, int64_t total_blocks) {
 
 cudaError_t launch_tc_kernel(int fmt, int bn, const TcArgs& a, const void* x_act, int64_t x_rows, int64_t x_k,
                              int grid, cudaStream_t stream);
+// Tensor map of a byte matrix (rows ld apart, ld a multiple of 16) for boxes of 128 bytes by box_rows
+// rows with the 128-byte swizzle; what lies outside reads as zero. False if it cannot be encoded.
+bool encode_bytes_2d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows);
 // R x as two bf16 planes [2][M][Kp] (hi, lo) in the decoded K order, for the prefill GEMM.
 // Token m is scaled by 2^-tok_ex[m] (tok_ex [M] int, written first by a per-token pass: the
 // exponent of the token's largest |x|), so that tiny and huge tokens keep full precision.

@@ -117,17 +117,17 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 
 // The channels are the rows of the MMA (A, 128 a CTA), the tokens its columns (B), so that a thread of the
 // epilogue owns one channel and a warp writes 32 neighbouring ones. A tile is 128 channels (256 for a
-// CTA pair) by tn tokens; its K is cut in blocks of 128 bytes, one stage of the ring each (TMA, 128-byte
-// swizzle, zeros behind the ends of K, M and N).
-// Work: worker c (a CTA or a pair) first takes blocks [c S / G, (c + 1) S / G) of the first sk_tiles
-// tiles (S blocks in all), then whole tiles sk_tiles + c, + G, ... A tile cut by a range's end is
-// finished by whichever of its workers comes last: each adds its int32 sums to the tile's in the
-// workspace (zero between calls), and the last reads them. The sums are exact, so the order of the
-// additions changes nothing.
-// Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 are the epilogue (TMEM lanes 32 (warp % 4) ..).
+// CTA pair) by tn tokens; its K is cut in blocks of 128 bytes, one stage of a ring each (TMA, 128-byte
+// swizzle, zeros behind the ends of K, M and N). Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 are the
+// epilogue (TMEM lanes 32 (warp % 4) ..). Every wait is bounded.
+//
+// Two forms (plan_gemm_i8 chooses by the time it expects of each):
+//   split  a cluster of `split` CTAs shares a tile, each with its part of K; they leave their int32 sums
+//          in shared memory and each finishes its part of the tokens from all of them. Two CTAs fit an SM.
+//   pair   persistent CTA pairs (cta_group::2): a pair loads each operand once for 256 x tn outputs, and
+//          the epilogue of a tile overlaps the products of the next (two accumulators).
 constexpr int kGemmThreads = 192;
-constexpr int kMaxStages = 10;
-constexpr int kSmemRing = 208 * 1024;
+constexpr int kMaxStages = 8;
 
 struct GemmBars {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
@@ -137,40 +137,46 @@ struct GemmBars {
 
 struct GemmParams {
   GemmI8Args a;
-  int tn, mt, kb, tiles, sk_tiles, stages, tmem_cols;
-  int* counter;      // one per epilogue warp of each worker's CTAs, zero between calls
-  int* partial;      // [worker][CTA of the pair][tn][128]: sums of the cut tile that starts in its range, zero between calls
+  int tn, mt, kb, tiles, split, stages, tmem_cols;
   int* err;
 };
 
-struct Piece {
-  int tile, k0, k1;
-};
-// The pieces of worker c in order.
-struct Pieces {
-  int u, u1, kb, next, tiles, G;
-  __device__ __forceinline__ Pieces(const GemmParams& p, int c, int G_) : kb(p.kb), tiles(p.tiles), G(G_) {
-    const int S = p.sk_tiles * p.kb;
-    u = (int)((int64_t)c * S / G);
-    u1 = (int)((int64_t)(c + 1) * S / G);
-    next = p.sk_tiles + c;
-  }
-  __device__ __forceinline__ bool get(Piece& o) {
-    if (u < u1) {
-      o.tile = u / kb;
-      o.k0 = u - o.tile * kb;
-      o.k1 = min(kb, o.k0 + (u1 - u));
-      u += o.k1 - o.k0;
-      return true;
+__device__ __forceinline__ void init_bars(GemmBars& bars, int stages, int empties) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
     }
-    if (next >= tiles) return false;
-    o.tile = next;
-    o.k0 = 0;
-    o.k1 = kb;
-    next += G;
-    return true;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], empties);
+    }
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+}
+
+// Position in the ring of stages.
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0, count = 0;
+  __device__ __forceinline__ void next(int stages) {
+    ++count;
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
+    }
   }
 };
+
+// On the way out of an aborted CTA: let the copies in flight land (bounded).
+__device__ __forceinline__ void drain(GemmBars& bars, const Ring& r, int stages) {
+  const uint32_t n = min(r.count, (uint32_t)stages);
+  for (uint32_t i = 1; i <= n; ++i) {
+    const uint32_t j = r.count - i;
+    if (!mbar_wait_drain(&bars.full[j % stages], (j / stages) & 1)) break;
+  }
+}
 
 // x_scale of 16 tokens (`left` of them real; the address is 64-byte aligned).
 __device__ __forceinline__ void load_scales16(const float* xs, int left, float v[16]) {
@@ -231,250 +237,275 @@ __device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, in
     if (i < left) y[i * a.ldy] = (uint16_t)h[i];
 }
 
-template <bool PAIR>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-    gemm_i8_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+// 16 tokens of one channel from their sums.
+__device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16], int m, int left, int ch, int lane, float ws, float bias) {
+  float xs[16], v[16];
+  load_scales16(a.x_scale + m, left, xs);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = (float)sum[i] * xs[i] * ws;
+  store16(a, m, left, ch, lane, v, bias);
+}
+
+// ---- split form: cluster rank r of tile t takes K blocks [r kb / split, (r + 1) kb / split)
+__global__ void __launch_bounds__(kGemmThreads, 2)
+    gemm_i8_split_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ GemmBars bars;
-  constexpr int CG = PAIR ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0;
-  const int worker = blockIdx.x / CG, G = gridDim.x / CG;
-  const int b_rows = p.tn / CG;                       // tokens that this CTA loads
-  const uint32_t a_bytes = 128 * 128, b_bytes = (uint32_t)b_rows * 128, stage_bytes = a_bytes + b_bytes;
+  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  const int rg = tile / p.mt, mt = tile - rg * p.mt;
+  const int n0 = rg * 128, m0 = mt * p.tn;
+  const int k0 = rank * p.kb / p.split, k1 = (rank + 1) * p.kb / p.split;
+  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)p.tn * 128;
   volatile int* abort_flag = &bars.abort_flag;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.acc_full[i], 1);
-      mbar_init(&bars.acc_empty[i], 4 * CG);
-    }
-    bars.abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 1) {
-    if (PAIR) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
-    else tmem_alloc(&bars.tmem_base, p.tmem_cols);
-  }
+  init_bars(bars, p.stages, 4);
+  if (warp == 1) tmem_alloc(&bars.tmem_base, p.tmem_cols);
   fence_before_sync();
-  if (PAIR) cluster_sync();
-  else __syncthreads();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = bars.tmem_base;
+  const int q = warp & 3, row = 32 * q + lane, ch = n0 + row;
+  const int cols = min(p.tn, p.a.M - m0);   // tokens of this tile
+  float ws = 0.f, bias = 0.f;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring r;
+      bool ok = true;
+      for (int k = k0; k < k1; ++k, r.next(p.stages)) {
+        if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 501))) break;
+        uint8_t* st = ring + r.s * stage_bytes;
+        mbar_arrive_expect_tx(&bars.full[r.s], stage_bytes);
+        tma_load_2d(st, &wmap, k * 128, n0, &bars.full[r.s]);
+        tma_load_2d(st + a_bytes, &xmap, k * 128, m0, &bars.full[r.s]);
+      }
+      if (!ok) drain(bars, r, p.stages);
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_i8s(128, p.tn);
+    Ring r;
+    bool ok = true;
+    for (int k = k0; k < k1; ++k, r.next(p.stages)) {
+      if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 503))) break;
+      fence_after_sync();
+      const uint8_t* st = ring + r.s * stage_bytes;
+      mma4_i8_ss_commit_elect<false>(tmem, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != k0, &bars.empty[r.s]);
+    }
+    if (ok) mma_commit_elect(&bars.acc_full[0]);
+  } else {
+    if (ch < p.a.N) {
+      ws = __ldg(p.a.w_scale + ch);
+      if (p.a.bias) bias = __ldg(p.a.bias + ch);
+    }
+    if (mbar_wait(&bars.acc_full[0], 0, abort_flag, p.err, 504)) {
+      fence_after_sync();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+      int* mine = reinterpret_cast<int*>(ring) + row;   // [token][channel]; every copy has been consumed
+      for (int c0 = 0; c0 < cols; c0 += 16) {
+        float v[16];
+        int sum[16];
+        tmem_ld16(acc + c0, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
+        if (p.split == 1) {
+          finish16(p.a, sum, m0 + c0, cols - c0, ch, lane, ws, bias);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(c0 + i) * 128] = sum[i];
+        }
+      }
+    }
+    fence_before_sync();
+  }
+  if (p.split > 1) {
+    cluster_sync();   // all parts are in shared memory
+    if (warp >= 2 && !*abort_flag) {
+      // groups of 16 tokens (one group at most 16): this CTA's are rank, rank + split, ... in steps of `g`
+      const int g = min(16, (cols + p.split - 1) / p.split);
+      for (int c0 = rank * g; c0 < cols; c0 += p.split * g) {
+        int sum[16] = {};
+        const int left = min(g, cols - c0);
+        for (int c = 0; c < p.split; ++c) {
+          const uint32_t src = cluster_addr(ring, c) + (uint32_t)(c0 * 128 + row) * 4;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < left) sum[i] += ld_cluster(src + i * 512);
+        }
+        finish16(p.a, sum, m0 + c0, left, ch, lane, ws, bias);
+      }
+    }
+    cluster_sync();   // nobody leaves while its shared memory is read
+  } else {
+    __syncthreads();
+  }
+  fence_after_sync();
+  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+}
+
+// ---- pair form
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    gemm_i8_pair_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ GemmBars bars;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int worker = blockIdx.x / 2, G = gridDim.x / 2;
+  const int b_rows = p.tn / 2;                       // tokens that this CTA loads
+  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)b_rows * 128;
+  volatile int* abort_flag = &bars.abort_flag;
+  init_bars(bars, p.stages, 8);
+  if (warp == 1) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
+  fence_before_sync();
+  cluster_sync();
   fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ loads
     if (lane == 0) {
-      prefetch_tensormap(&wmap);
-      prefetch_tensormap(&xmap);
-      uint32_t it = 0;
-      int s = 0;
-      uint32_t ph = 0;
+      Ring r;
       bool ok = true;
-      Pieces pieces(p, worker, G);
-      for (Piece w; ok && pieces.get(w);) {
-        const int rg = w.tile / p.mt, mt = w.tile - rg * p.mt;
-        const int n0 = (rg * CG + (int)rank) * 128, m0 = mt * p.tn + (int)rank * b_rows;
-        for (int k = w.k0; k < w.k1; ++k) {
-          if (!(ok = mbar_wait_bg(&bars.empty[s], ph ^ 1, abort_flag, p.err, 501))) break;
-          uint8_t* a_st = ring + s * stage_bytes;
-          if (PAIR) {
-            // both CTAs' copies complete on the leader's barrier
-            if (rank == 0) mbar_arrive_expect_tx(&bars.full[s], 2 * stage_bytes);
-            const uint32_t bar = cluster_addr(&bars.full[s], 0);
-            tma_load_2d_pair(a_st, &wmap, k * 128, n0, bar);
-            tma_load_2d_pair(a_st + a_bytes, &xmap, k * 128, m0, bar);
-          } else {
-            mbar_arrive_expect_tx(&bars.full[s], stage_bytes);
-            tma_load_2d(a_st, &wmap, k * 128, n0, &bars.full[s]);
-            tma_load_2d(a_st + a_bytes, &xmap, k * 128, m0, &bars.full[s]);
-          }
-          ++it;
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1;
-          }
+      for (int t = worker; ok && t < p.tiles; t += G) {
+        const int rg = t / p.mt, mt = t - rg * p.mt;
+        const int n0 = (rg * 2 + (int)rank) * 128, m0 = mt * p.tn + (int)rank * b_rows;
+        for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
+          if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 511))) break;
+          uint8_t* st = ring + r.s * stage_bytes;
+          // both CTAs' copies complete on the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[r.s], 2 * stage_bytes);
+          const uint32_t bar = cluster_addr(&bars.full[r.s], 0);
+          tma_load_2d_pair(st, &wmap, k * 128, n0, bar);
+          tma_load_2d_pair(st + a_bytes, &xmap, k * 128, m0, bar);
         }
       }
-      if (!ok && rank == 0) {   // let the copies in flight land before the CTA leaves
-        const uint32_t n = it < (uint32_t)p.stages ? it : (uint32_t)p.stages;
-        for (uint32_t i = 0; i < n; ++i) {
-          const uint32_t j = it - 1 - i;
-          if (!mbar_wait_drain(&bars.full[j % p.stages], (j / p.stages) & 1)) break;
-        }
-      }
+      if (!ok && rank == 0) drain(bars, r, p.stages);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (the pair's leader)
-    if (rank == 0) {
-      const uint32_t idesc = idesc_i8s(128 * CG, p.tn);
-      int s = 0;
-      uint32_t ph = 0, n = 0;
+    if (rank == 0) {   // the leader issues for both CTAs
+      const uint32_t idesc = idesc_i8s(256, p.tn);
+      Ring r;
+      uint32_t n = 0;
       bool ok = true;
-      Pieces pieces(p, worker, G);
-      for (Piece w; ok && pieces.get(w); ++n) {
+      for (int t = worker; ok && t < p.tiles; t += G, ++n) {
         const uint32_t d = n & 1;
-        if (!(ok = mbar_wait_bg(&bars.acc_empty[d], ((n >> 1) & 1) ^ 1, abort_flag, p.err, 502))) break;
-        for (int k = w.k0; k < w.k1; ++k) {
-          if (!(ok = mbar_wait_bg(&bars.full[s], ph, abort_flag, p.err, 503))) break;
+        if (!(ok = mbar_wait(&bars.acc_empty[d], ((n >> 1) & 1) ^ 1, abort_flag, p.err, 512))) break;
+        fence_after_sync();
+        for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
+          if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 513))) break;
           fence_after_sync();
-          const uint8_t* a_st = ring + s * stage_bytes;
-          mma4_i8_ss_commit_elect<PAIR>(tmem + d * p.tn, smem_desc_sw128(a_st), smem_desc_sw128(a_st + a_bytes), idesc, k != w.k0,
-                                        &bars.empty[s]);
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1;
-          }
+          const uint8_t* st = ring + r.s * stage_bytes;
+          mma4_i8_ss_commit_elect<true>(tmem + d * p.tn, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != 0,
+                                        &bars.empty[r.s]);
         }
-        if (!ok) break;
-        if (PAIR) mma_commit_pair_elect(&bars.acc_full[d]);
-        else mma_commit_elect(&bars.acc_full[d]);
+        if (ok) mma_commit_pair_elect(&bars.acc_full[d]);
       }
     }
   } else {
-    // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int S = p.sk_tiles * p.kb;
     uint32_t n = 0;
-    Pieces pieces(p, worker, G);
-    for (Piece w; pieces.get(w); ++n) {
+    for (int t = worker; t < p.tiles; t += G, ++n) {
       const uint32_t d = n & 1;
-      const int rg = w.tile / p.mt, mt = w.tile - rg * p.mt;
-      const int ch = (rg * CG + (int)rank) * 128 + 32 * q + lane, m0 = mt * p.tn;
+      const int rg = t / p.mt, mt = t - rg * p.mt;
+      const int ch = (rg * 2 + (int)rank) * 128 + 32 * q + lane, m0 = mt * p.tn;
       const int cols = min(p.tn, p.a.M - m0);         // tokens of this tile
       const float ws = ch < p.a.N ? __ldg(p.a.w_scale + ch) : 0.f;
       const float bias = p.a.bias && ch < p.a.N ? __ldg(p.a.bias + ch) : 0.f;
-      if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 504)) break;
+      if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
       fence_after_sync();
       const uint32_t acc = tmem + d * p.tn + ((uint32_t)(32 * q) << 16);
-      auto release = [&]() {   // the accumulator may be overwritten
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[d], 0));
-          else mbar_arrive(&bars.acc_empty[d]);
-        }
-      };
-      if (w.k0 == 0 && w.k1 == p.kb) {
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16];
-          tmem_ld16(acc + c0, v);
-          float xs[16];
-          load_scales16(p.a.x_scale + m0 + c0, cols - c0, xs);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = (float)__float_as_int(v[i]) * xs[i] * ws;
-          store16(p.a, m0 + c0, cols - c0, ch, lane, v, bias);
-        }
-        release();
-        continue;
-      }
-      // a piece of a tile: add it to the tile's sums in the workspace; the last piece to arrive writes y
-      const int tb = w.tile * p.kb;
-      const int c_first = (int)((((int64_t)tb + 1) * G - 1) / S), c_last = (int)(((int64_t)(tb + p.kb) * G - 1) / S);
-      int* sums = p.partial + ((int64_t)c_first * CG + rank) * p.tn * 128 + 32 * q + lane;
       for (int c0 = 0; c0 < cols; c0 += 16) {
         float v[16];
+        int sum[16];
         tmem_ld16(acc + c0, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) atomicAdd(sums + (c0 + i) * 128, __float_as_int(v[i]));
+        for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
+        finish16(p.a, sum, m0 + c0, cols - c0, ch, lane, ws, bias);
       }
-      release();
-      __threadfence();
+      fence_before_sync();
       __syncwarp();
-      int* counter = p.counter + (c_first * CG + (int)rank) * 4 + q;
-      int seen = 0;
-      if (lane == 0) seen = atomicAdd(counter, 1);
-      seen = __shfl_sync(0xffffffffu, seen, 0);
-      if (seen != c_last - c_first) continue;
-      __threadfence();
-      if (lane == 0) *counter = 0;
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        int t[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) t[i] = c0 + i < p.tn ? __ldcg(sums + (c0 + i) * 128) : 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c0 + i < p.tn) __stcg(sums + (c0 + i) * 128, 0);
-#pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-          if (c0 + h >= cols) break;
-          float v[16], xs[16];
-          load_scales16(p.a.x_scale + m0 + c0 + h, cols - c0 - h, xs);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = (float)t[h + i] * xs[i] * ws;
-          store16(p.a, m0 + c0 + h, cols - c0 - h, ch, lane, v, bias);
-        }
-      }
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[d], 0));
     }
   }
   fence_before_sync();
-  if (PAIR) cluster_sync();
-  else __syncthreads();
+  cluster_sync();
   fence_after_sync();
-  if (warp == 1) {
-    if (PAIR) tmem_dealloc_pair(tmem, p.tmem_cols);
-    else tmem_dealloc(tmem, p.tmem_cols);
-  }
+  if (warp == 1) tmem_dealloc_pair(tmem, p.tmem_cols);
 }
 
-constexpr int kGemmSmem = kSmemRing + 1024;
 constexpr int kSMs = 148;
+constexpr int kSplitRing = 96 * 1024, kPairRing = 208 * 1024;   // two split CTAs, or one of a pair, fill an SM
 
-template <bool PAIR>
-cudaError_t run_gemm(const GemmParams& p, int workers, const CUtensorMap& wmap, const CUtensorMap& xmap, cudaStream_t stream) {
-  // per device: an attribute set on one does not hold on another
-  const cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+// Shared memory limits are set once per device and kernel.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, bool* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(workers * (PAIR ? 2 : 1)));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  if (PAIR) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  return cudaLaunchKernelEx(&cfg, gemm_i8_kernel<PAIR>, p, wmap, xmap);
+  return cudaSuccess;
 }
-
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// Expected times, in clocks of one SM. A block of 128 channels x tn tokens x 128 bytes of K takes
+// 2 tn clocks of the tensor core (8192 products a clock) and its operands come from L2 at about
+// kL2Bytes a clock; a tile has a start and an end (pipeline fill, epilogue, for a split tile the
+// exchange of sums), kTileClocks and 8 a token.
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
   *p = GemmI8Plan{};
-  p->pair = 0;
-  const int cg = 1, step = 16;
-  const int64_t mt = (M + 255) / 256;
-  p->tn = (int)(((M + mt - 1) / mt + step - 1) / step * step);
-  const int64_t tiles = mt * ((N + 128 * cg - 1) / (128 * cg));
-  if (tiles > (1 << 30)) return false;
-  p->mt = (int)mt;
-  p->tiles = (int)tiles;
-  p->kb = (int)((K + 127) / 128);
-  const int slots = kSMs / cg;
-  p->workers = (int)std::min<int64_t>(slots, tiles * p->kb);
-  const int64_t waves = tiles / p->workers, rest = tiles % p->workers;
-  if (rest != 0) p->sk_tiles = (int)(rest + (waves > 0 ? p->workers : 0));
-  if (p->sk_tiles > 0) {
-    p->counter_bytes = align256((size_t)p->workers * cg * 4 * sizeof(int));
-    p->workspace_bytes = p->counter_bytes + (size_t)p->workers * cg * p->tn * 128 * sizeof(int);
+  const int kb = (int)((K + 127) / 128);
+  p->kb = kb;
+  double best = 0;
+  constexpr double kL2Bytes = 48;
+  const int64_t mt0 = (M + 255) / 256, mt1 = std::min<int64_t>((M + 15) / 16, mt0 + 7);
+  for (int64_t mt = mt0; mt <= mt1; ++mt) {
+    {
+      const int tn = (int)(((M + mt - 1) / mt + 15) / 16 * 16);
+      const int64_t tiles = (M + tn - 1) / tn * ((N + 127) / 128);
+      if (tiles > (1 << 26)) return false;
+      const double block = std::max(2.0 * tn, (16384 + 128.0 * tn) / kL2Bytes);
+      for (int s = 1; s <= std::min(8, kb); ++s) {
+        const int64_t rounds = (tiles * s + kSMs - 1) / kSMs;
+        const double t = rounds * ((kb + s - 1) / s) * block + (rounds + 1) / 2 * (1500 + 8.0 * tn) + (s > 1 ? 800 + 4.0 * tn : 0);
+        if (p->tn == 0 || t < best) {
+          best = t;
+          p->pair = 0;
+          p->tn = tn;
+          p->mt = (int)((M + tn - 1) / tn);
+          p->tiles = (int)tiles;
+          p->split = s;
+          p->workers = (int)tiles;
+        }
+      }
+    }
+    if (N > 128 && M > 32) {
+      const int tn = (int)(((M + mt - 1) / mt + 31) / 32 * 32);
+      const int64_t tiles = (M + tn - 1) / tn * ((N + 255) / 256);
+      const double block = std::max(2.0 * tn, (16384 + 64.0 * tn) / kL2Bytes);
+      const int64_t rounds = (tiles + kSMs / 2 - 1) / (kSMs / 2);
+      const double t = rounds * std::max((double)kb * block, 500 + 12.0 * tn) + 2000 + 12.0 * tn;
+      if (t < best) {
+        best = t;
+        p->pair = 1;
+        p->tn = tn;
+        p->mt = (int)((M + tn - 1) / tn);
+        p->tiles = (int)tiles;
+        p->split = 1;
+        p->workers = (int)std::min<int64_t>(tiles, kSMs / 2);
+      }
+    }
   }
   return true;
 }
 
-cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, void* workspace, int* err, cudaStream_t stream) {
+cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, cudaStream_t stream) {
   const int cg = pl.pair ? 2 : 1;
   GemmParams p{};
   p.a = a;
@@ -482,17 +513,34 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, void* work
   p.mt = pl.mt;
   p.kb = pl.kb;
   p.tiles = pl.tiles;
-  p.sk_tiles = pl.sk_tiles;
-  p.stages = std::min(kMaxStages, kSmemRing / (128 * 128 + pl.tn / cg * 128));
+  p.split = pl.split;
+  const int stage = 128 * 128 + pl.tn / cg * 128;
+  p.stages = std::min(kMaxStages, (pl.pair ? kPairRing : kSplitRing) / stage);
   p.tmem_cols = 32;
-  while (p.tmem_cols < 2 * pl.tn) p.tmem_cols *= 2;
-  p.counter = static_cast<int*>(workspace);
-  p.partial = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + pl.counter_bytes);
+  while (p.tmem_cols < cg * pl.tn) p.tmem_cols *= 2;   // two accumulators in the pair form
   p.err = err;
   CUtensorMap wmap, xmap;
   if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg))
     return cudaErrorInvalidValue;
-  return pl.pair ? run_gemm<true>(p, pl.workers, wmap, xmap, stream) : run_gemm<false>(p, pl.workers, wmap, xmap, stream);
+  static bool split_done[64], pair_done[64];
+  cudaError_t e = pl.pair ? allow_smem(gemm_i8_pair_kernel, kPairRing + 1024, pair_done)
+                          : allow_smem(gemm_i8_split_kernel, 128 * 1024 + 1024, split_done);
+  if (e != cudaSuccess) return e;
+  // the ring, or the sums that replace it at the end of a split tile
+  const int ring = pl.pair ? kPairRing : std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pl.workers * (pl.pair ? 2 : pl.split)));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = (size_t)ring + 1024;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = pl.pair ? 2 : (unsigned)pl.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return pl.pair ? cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel, p, wmap, xmap)
+                 : cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel, p, wmap, xmap);
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {

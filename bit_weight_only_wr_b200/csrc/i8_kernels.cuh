@@ -38,20 +38,19 @@ struct GemmI8Args {
 };
 // The work of one call on the tensor cores, planned on the host (see gemm_i8.cu).
 struct GemmI8Plan {
-  int pair;        // 1: CTA pairs (256 channels a tile), 0: single CTAs (128)
+  int pair;        // 1: CTA pairs (256 channels a tile), 0: clusters of `split` CTAs (128)
   int tn;          // tokens a tile
   int mt;          // token tiles
   int kb;          // 128-byte blocks of K
-  int workers;     // CTAs, or pairs
+  int split;       // CTAs that share a tile's K
   int tiles;
-  int sk_tiles;    // the first sk_tiles tiles are cut along K into one range of blocks per worker
-  size_t counter_bytes, workspace_bytes;
+  int workers;     // pairs, or clusters, of the launch
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
 // Tokens up to which the product runs on dp4a, without a workspace.
 constexpr int kGemvI8Tokens = 8;
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);
-cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, void* workspace, int* err, cudaStream_t stream);
+cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream);
 // Sums of K products of int8 values stay inside int32 up to this K ((-128)^2 * K < 2^31).
 constexpr int64_t kMaxI8K = 131071;
 

@@ -19,19 +19,53 @@
 namespace wr {
 namespace {
 
-// ---------------------------------------------------------------- loads and stores of 8 elements
+// ---------------------------------------------------------------- two fp32 operations in one instruction
 
-// Eight elements as loaded: 16 bytes of a 16-bit type (a), 32 bytes of fp32 (a, b). Loads are issued
-// for all operands of a row before the first is converted, so they are kept raw.
-struct Raw8 {
-  uint32_t r[8];
+// These kernels are short of instruction slots before they are short of bandwidth, and sm_100a has
+// packed fp32 multiply, add and multiply-add (each half rounded as the plain one).
+struct f32x2 {
+  uint64_t v;
+};
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ f32x2 splat2(float v) { return pack2(v, v); }
+// A thread's vector: 8 elements as 4 pairs.
+struct Vec8 {
+  f32x2 p[4];
 };
 
-__device__ __forceinline__ uint4 ld16(const uint8_t* p, bool pred) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-               : "l"(p), "r"((int)pred));
+// ---------------------------------------------------------------- loads and stores of 8 elements
+
+// Eight elements as loaded: 32 bytes of fp32, 16 of a 16-bit type. Loads are issued for all operands of a
+// row before the first is converted, so they are kept raw. The size is a template parameter (a raw
+// vector has to stay in registers), bf16 or fp16 is decided when it is converted.
+template <bool F32>
+struct Raw8 {
+  uint32_t r[F32 ? 8 : 4];
+};
+
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -42,59 +76,58 @@ __device__ __forceinline__ int elem(int i, int j, int T, int t) {
   return VEC ? (i * T + t) * 8 + j : (i * 8 + j) * T + t;
 }
 
-template <bool VEC>
-__device__ __forceinline__ Raw8 load8(const uint8_t* row, int type, int i, int T, int t, int D) {
-  Raw8 v;
-  const bool f32 = type == WR_F32;
-  if (VEC) {
-    const int e = elem<true>(i, 0, T, t);
-    const bool whole = e + 8 <= D;
-    const uint8_t* p = row + (int64_t)e * (f32 ? 4 : 2);
-    const uint4 a = ld16(p, whole), b = ld16(p + 16, whole && f32);
+// Vector i of thread t; zero past the row's D elements.
+template <bool F32, bool VEC>
+__device__ __forceinline__ Raw8<F32> load8(const uint8_t* row, int i, int T, int t, int D) {
+  Raw8<F32> v;
+  const int e0 = elem<VEC>(i, 0, T, t);
+  if (VEC && e0 + 8 <= D) {
+    const uint8_t* p = row + (int64_t)e0 * (F32 ? 4 : 2);
+    const uint4 a = ld16(p);
     v.r[0] = a.x; v.r[1] = a.y; v.r[2] = a.z; v.r[3] = a.w;
-    v.r[4] = b.x; v.r[5] = b.y; v.r[6] = b.z; v.r[7] = b.w;
-    if (!whole && e < D) {   // the row's last vector
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (e + j < D) {
-          if (f32) v.r[j] = reinterpret_cast<const uint32_t*>(row)[e + j];
-          else v.r[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[e + j] << (16 * (j & 1));
-        }
-      }
+    if constexpr (F32) {
+      const uint4 b = ld16(p + 16);
+      v.r[4] = b.x; v.r[5] = b.y; v.r[6] = b.z; v.r[7] = b.w;
     }
-  } else {
+    return v;
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v.r[j] = 0;
+  for (int j = 0; j < (F32 ? 8 : 4); ++j) v.r[j] = 0;
+  if (e0 >= D) return v;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = elem<false>(i, j, T, t);
-      if (e < D) {
-        if (f32) v.r[j] = reinterpret_cast<const uint32_t*>(row)[e];
-        else v.r[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[e] << (16 * (j & 1));
-      }
+  for (int j = 0; j < 8; ++j) {
+    const int e = elem<VEC>(i, j, T, t);
+    if (e < D) {
+      if constexpr (F32) v.r[j] = reinterpret_cast<const uint32_t*>(row)[e];
+      else v.r[j / 2] |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[e] << (16 * (j & 1));
     }
   }
   return v;
 }
 
-__device__ __forceinline__ void to_float8(const Raw8& v, int type, float f[8]) {
-  if (type == WR_F32) {
+template <bool F32>
+__device__ __forceinline__ Vec8 to_float8(const Raw8<F32>& v, int type) {
+  Vec8 f;
+  if constexpr (F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v.r[j]);
+    for (int j = 0; j < 4; ++j) f.p[j] = pack2(__uint_as_float(v.r[2 * j]), __uint_as_float(v.r[2 * j + 1]));
   } else if (type == WR_BF16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(v.r[j] << 16);
-      f[2 * j + 1] = __uint_as_float(v.r[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < 4; ++j) f.p[j] = pack2(__uint_as_float(v.r[j] << 16), __uint_as_float(v.r[j] & 0xFFFF0000u));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&v.r[j]));
-      f[2 * j] = h.x;
-      f[2 * j + 1] = h.y;
+      f.p[j] = pack2(h.x, h.y);
     }
   }
+  return f;
+}
+// The same where the type's size is not a template parameter.
+template <bool VEC>
+__device__ __forceinline__ Vec8 load_float8(const void* row, int type, int i, int T, int t, int D) {
+  const uint8_t* p = static_cast<const uint8_t*>(row);
+  return type == WR_F32 ? to_float8(load8<true, VEC>(p, i, T, t, D), type) : to_float8(load8<false, VEC>(p, i, T, t, D), type);
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
@@ -108,7 +141,10 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int type) {
 
 // Rounds to nearest even (fp16 beyond 65504 gives infinity, as the type does).
 template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t* row, int type, int i, int T, int t, int D, const float f[8]) {
+__device__ __forceinline__ void store8(uint8_t* row, int type, int i, int T, int t, int D, const Vec8& v) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack2(v.p[j], f[2 * j], f[2 * j + 1]);
   uint32_t p[4];
   if (type != WR_F32) {
 #pragma unroll
@@ -139,20 +175,23 @@ __device__ __forceinline__ void store8(uint8_t* row, int type, int i, int T, int
 
 // Every warp leaves its value in buf and every thread reads all of them: one barrier for each
 // reduction (each has its own buf). The sum runs in the same order in every thread and every run.
-__device__ __forceinline__ float row_sum(float v, float* buf) {
+__device__ __forceinline__ float row_sum(f32x2 v2, float* buf) {
+  float v, hi;
+  unpack2(v2, v, hi);
+  v += hi;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int nw = blockDim.x >> 5;
   if (nw == 1) return v;
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = (threadIdx.x & 31) < nw ? buf[threadIdx.x & 31] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  float s = 0.f;
+  for (int i = 0; i < nw; ++i) s += buf[i];
   return s;
 }
 // Largest magnitude, by its bits: an infinity is above every number and a NaN above that.
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
+__device__ __forceinline__ uint32_t row_max(float amax, uint32_t* buf) {
+  uint32_t v = __float_as_uint(amax) & 0x7FFFFFFFu;
   v = __reduce_max_sync(0xffffffffu, v);
   const int nw = blockDim.x >> 5;
   if (nw == 1) return v;
@@ -160,16 +199,36 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf) {
   __syncthreads();
   return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < nw ? buf[threadIdx.x & 31] : 0u);
 }
+// max(a, |v|), NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(v)));
+  return r;
+}
+__device__ __forceinline__ float max_abs8(float a, const Vec8& v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    unpack2(v.p[j], lo, hi);
+    a = max_abs(max_abs(a, lo), hi);
+  }
+  return a;
+}
 
 // ---------------------------------------------------------------- the 8-bit rounding
 
 // Codes of one row with largest magnitude A: the integer nearest to 127 v / A, a tie to the even one,
 // decided on the exact quotient. t = v * fl(127 / A) is off by at most 127 * 2^-23 < 1.6e-5 (two
 // roundings of at most 2^-24 relative each), so only a value that close to the middle of two codes
-// needs more: there the quotient is formed in fp64. The 31-bit product 127 v is exact in fp64, a tie's
-// quotient is exact too, and any other quotient is at least 2^-40 (relative) away from a tie.
+// needs more. There the sign of 127 v - (k + 1/2) A decides, k = floor(t): both products are taken as a
+// rounded part and its exact rest (31 and 32 bits: the rests have at most 8), the rounded parts are
+// close enough to subtract exactly, and so are the rests. 16-bit inputs have such values in every
+// third warp (v = A / 2 is one); with an fp64 division instead the quantizer of 9728 x 2560 bf16
+// values took 46.5 us instead of 31.3.
 // A = 0: codes 0 and scale 0. A not finite (an infinity or NaN in the row): codes 0 and scale NaN, so
-// that whatever is computed from the row is NaN. Below 2^-100 fl(127 / A) could overflow: all in fp64.
+// that whatever is computed from the row is NaN. Where A is so small or large that 127 / A, 127 v or a
+// rest leaves the fp32 range (`wide`), the quotient is formed in fp64: 127 v and a tie's quotient are
+// exact there, and any other quotient is at least 2^-40 (relative) away from a tie.
 struct RowCode {
   float A, inv, scale;
   bool wide;
@@ -178,26 +237,63 @@ __device__ __forceinline__ RowCode row_code(uint32_t amax_bits) {
   RowCode c;
   c.A = __uint_as_float(amax_bits);
   const bool finite = amax_bits < 0x7F800000u;
-  c.wide = finite && c.A > 0.f && c.A < 7.8886090522e-31f;
+  c.wide = finite && c.A > 0.f && (c.A < 0x1p-100f || c.A > 0x1p+120f);
   c.inv = finite && c.A > 0.f && !c.wide ? __fdiv_rn(127.f, c.A) : 0.f;
   c.scale = finite ? __fdiv_rn(c.A, 127.f) : __uint_as_float(0x7FC00000u);
   if (!finite) c.A = 0.f;
   return c;
 }
 __device__ __noinline__ float code_exact(float v, float A) { return (float)rint((double)v * 127.0 / (double)A); }
-__device__ __forceinline__ int code_of(const RowCode& c, float v) {
-  if (c.A == 0.f) return 0;
-  const float t = v * c.inv;
-  float r = rintf(t);
-  if (c.wide || fabsf(fabsf(t - r) - 0.5f) < 2e-5f) r = code_exact(v, c.A);
-  return (int)r;
+// The codes of 8 values, a byte each. Adding 1.5 * 2^23 rounds t to the nearest integer (ties to even)
+// and leaves it, as two's complement, in the low bits.
+__device__ __forceinline__ void codes8(const RowCode& c, const Vec8& v, uint32_t p[2]) {
+  constexpr float kMagic = 12582912.f;
+  if (c.A == 0.f) {
+    p[0] = p[1] = 0;
+    return;
+  }
+  const f32x2 inv = splat2(c.inv), magic = splat2(kMagic), unmagic = splat2(-kMagic), minus = splat2(-1.f);
+  float r[8], far = 0.f;   // far: the largest distance from a code, of 1/2 at most
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 t = mul2(v.p[j], inv), rr = add2(t, magic);
+    const f32x2 d = fma2(t, minus, add2(rr, unmagic));
+    unpack2(rr, r[2 * j], r[2 * j + 1]);
+    float lo, hi;
+    unpack2(d, lo, hi);
+    far = fmaxf(fmaxf(far, fabsf(lo)), fabsf(hi));
+  }
+  if (far > 0.49998f || c.wide) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2(v.p[j], f[2 * j], f[2 * j + 1]);
+    if (c.wide) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = code_exact(f[j], c.A) + kMagic;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float k = floorf(__fmul_rn(f[j], c.inv)), h = k + 0.5f;
+        const float v1 = __fmul_rn(127.f, f[j]), v0 = __fmaf_rn(127.f, f[j], -v1);
+        const float a1 = __fmul_rn(h, c.A), a0 = __fmaf_rn(h, c.A, -a1);
+        const float d = __fadd_rn(__fsub_rn(v1, a1), __fsub_rn(v0, a0));
+        // a tie: k or k + 1, whichever is even (kMagic + h rounds to even)
+        r[j] = d > 0.f ? k + 1.f + kMagic : d < 0.f ? k + kMagic : h + kMagic;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __byte_perm(__float_as_uint(r[4 * h]), __float_as_uint(r[4 * h + 1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(r[4 * h + 2]), __float_as_uint(r[4 * h + 3]), 0x0040);
+    p[h] = __byte_perm(lo, hi, 0x5410);
+  }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_codes8(int8_t* row, int i, int T, int t, int D, const RowCode& c, const float f[8]) {
-  uint32_t p[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) p[j / 4] |= (uint32_t)(code_of(c, f[j]) & 0xFF) << (8 * (j & 3));
+__device__ __forceinline__ void store_codes8(int8_t* row, int i, int T, int t, int D, const RowCode& c, const Vec8& v) {
+  uint32_t p[2];
+  codes8(c, v, p);
   const int e0 = elem<VEC>(i, 0, T, t);
   if (VEC && e0 + 8 <= D) {
     *reinterpret_cast<uint2*>(row + e0) = make_uint2(p[0], p[1]);
@@ -210,185 +306,185 @@ __device__ __forceinline__ void store_codes8(int8_t* row, int i, int T, int t, i
   }
 }
 
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + expf(-g)); }
+// silu(g) x = g x / (1 + 2^(-g log2 e)), off by less than 9 * 2^-24: the exponent t = -g log2 e rounds to
+// t, and what it lost, r, comes back as a first-order term (2^(t + r) = 2^t (1 + r ln 2)); 2^t is off by at
+// most 2^-22.5 and the reciprocal by 2^-23 (the approximate instructions). t is held below 2^126 so that
+// an overflow cannot meet a zero: there silu is below 1e-36 and reads as 0.
+__device__ __forceinline__ Vec8 silu_mul(const Vec8& g, const Vec8& x) {
+  const f32x2 kLog2e = splat2(-1.4426950408889634f), kLn2 = splat2(0.6931471805599453f), kOne = splat2(1.f);
+  Vec8 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f32x2 t = mul2(g.p[j], kLog2e);
+    float lo, hi, elo, ehi;
+    unpack2(t, lo, hi);
+    lo = fminf(lo, 126.f);
+    hi = fminf(hi, 126.f);
+    t = pack2(-lo, -hi);
+    const f32x2 r = fma2(g.p[j], kLog2e, t);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(elo) : "f"(lo));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ehi) : "f"(hi));
+    const f32x2 e = pack2(elo, ehi);
+    const f32x2 s = fma2(mul2(e, r), kLn2, add2(e, kOne));
+    unpack2(s, lo, hi);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(elo) : "f"(lo));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ehi) : "f"(hi));
+    o.p[j] = mul2(mul2(g.p[j], pack2(elo, ehi)), x.p[j]);
+  }
+  return o;
+}
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__host__ __device__ inline int type_bytes(int type) { return type == WR_F32 ? 4 : (type == WR_I8 ? 1 : 2); }
 
 // ---------------------------------------------------------------- row quantizer
 
 // VPT > 0: the row stays in registers. VPT = 0: rows longer than that; read twice (the second time
-// mostly from L2), VEC in steps of one vector.
-template <int VPT, int MAXT, bool VEC>
+// mostly from L2), in steps of one vector a thread.
+template <int VPT, int MAXT, bool VEC, bool F32, bool GATED>
 __global__ void __launch_bounds__(MAXT) quantize_rows_kernel(const QuantRowsArgs a) {
   __shared__ uint32_t buf[32];
   const int T = blockDim.x, t = threadIdx.x;
-  const int64_t m = blockIdx.x;
-  const int es = a.type == WR_F32 ? 4 : 2;
+  const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (m >= a.M) return;   // (whole warps)
+  constexpr int es = F32 ? 4 : 2;
   const uint8_t* x = a.x + m * a.ldx * es;
-  const uint8_t* g = a.gate ? a.gate + m * a.ldg * es : nullptr;
+  const uint8_t* g = GATED ? a.gate + m * a.ldg * es : nullptr;
   int8_t* q = a.q + m * a.ldq;
-  auto values = [&](const Raw8& rx, const Raw8& rg, float f[8]) {
-    to_float8(rx, a.type, f);
-    if (g) {
-      float gf[8];
-      to_float8(rg, a.type, gf);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= silu(gf[j]);
-    }
-  };
-  uint32_t amax = 0;
+  float amax = 0.f;
   if constexpr (VPT > 0) {
-    Raw8 rx[VPT], rg[VPT];
+    Raw8<F32> rx[VPT], rg[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      rx[i] = load8<VEC>(x, a.type, i, T, t, a.K);
-      if (g) rg[i] = load8<VEC>(g, a.type, i, T, t, a.K);
+      rx[i] = load8<F32, VEC>(x, i, T, t, a.K);
+      if (GATED) rg[i] = load8<F32, VEC>(g, i, T, t, a.K);
     }
-    float f[VPT][8];
+    Vec8 v[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      values(rx[i], rg[i], f[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(f[i][j]));
+      v[i] = to_float8(rx[i], a.type);
+      if (GATED) v[i] = silu_mul(to_float8(rg[i], a.type), v[i]);
+      amax = max_abs8(amax, v[i]);
     }
     const RowCode c = row_code(row_max(amax, buf));
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) store_codes8<VEC>(q, i, T, t, a.K, c, f[i]);
+    for (int i = 0; i < VPT; ++i) store_codes8<VEC>(q, i, T, t, a.K, c, v[i]);
     if (t == 0) a.scale[m] = c.scale;
   } else {
     const int steps = (a.K + 8 * T - 1) / (8 * T);
-    float f[8];
-    for (int i = 0; i < steps; ++i) {
-      const Raw8 rx = load8<VEC>(x, a.type, i, T, t, a.K);
-      Raw8 rg = rx;
-      if (g) rg = load8<VEC>(g, a.type, i, T, t, a.K);
-      values(rx, rg, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(f[j]));
-    }
+    auto step = [&](int i) {
+      const Raw8<F32> rx = load8<F32, VEC>(x, i, T, t, a.K);
+      if (!GATED) return to_float8(rx, a.type);
+      return silu_mul(to_float8(load8<F32, VEC>(g, i, T, t, a.K), a.type), to_float8(rx, a.type));
+    };
+#pragma unroll 2
+    for (int i = 0; i < steps; ++i) amax = max_abs8(amax, step(i));
     const RowCode c = row_code(row_max(amax, buf));
-    for (int i = 0; i < steps; ++i) {
-      const Raw8 rx = load8<VEC>(x, a.type, i, T, t, a.K);
-      Raw8 rg = rx;
-      if (g) rg = load8<VEC>(g, a.type, i, T, t, a.K);
-      values(rx, rg, f);
-      store_codes8<VEC>(q, i, T, t, a.K, c, f);
-    }
+    for (int i = 0; i < steps; ++i) store_codes8<VEC>(q, i, T, t, a.K, c, step(i));
     if (t == 0) a.scale[m] = c.scale;
   }
 }
 
 // ---------------------------------------------------------------- residual + norm
 
-__host__ __device__ inline int type_bytes(int type) { return type == WR_F32 ? 4 : (type == WR_I8 ? 1 : 2); }
+// B32, R32, W32: whether the block, the residual, and the weights (the gate is usually like them) are fp32.
+struct NormArgs {
+  wr_residual_norm_args p;
+  float inv_d;           // 1 / D
+};
 
-template <int VPT, int MAXT, bool VEC>
-__global__ void __launch_bounds__(MAXT) residual_norm_kernel(const wr_residual_norm_args a) {
+template <int VPT, int MAXT, bool VEC, bool B32, bool R32, bool W32>
+__global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) {
+  const wr_residual_norm_args& a = na.p;
   __shared__ float buf_post[32], buf_norm[32];
   __shared__ uint32_t buf_max[32];
   const int T = blockDim.x, t = threadIdx.x, D = (int)a.D;
-  const int64_t m = blockIdx.x;
-  auto row_of = [&](const void* p, int64_t ld, int type) {
-    return static_cast<const uint8_t*>(p) + m * ld * type_bytes(type);
-  };
-  const uint8_t* b = a.block ? row_of(a.block, a.ld_block, a.block_type) : nullptr;
-  const uint8_t* h = a.residual ? row_of(a.residual, a.ld_residual, a.residual_type) : nullptr;
-  const uint8_t* g = a.gate ? row_of(a.gate, a.ld_gate, a.gate_type) : nullptr;
-  const float inv_d = 1.f / (float)D;
-  float v[VPT][8];   // the block's output, then h'
-  // the row itself is loaded at once; the gate and the weights too where the registers allow it
-  // (otherwise when they are used: they are the same for all rows and come from L2)
-  constexpr bool kEarly = VPT == 1;
-  Raw8 rb[VPT], rh[VPT], rg[VPT], rp[VPT], rn[VPT];
-  const uint8_t* pw = static_cast<const uint8_t*>(a.post_norm ? a.post_weight : nullptr);
-  const uint8_t* nw = static_cast<const uint8_t*>(a.y ? a.norm_weight : nullptr);
+  const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (m >= a.M) return;   // (whole warps)
+  const uint8_t* b = static_cast<const uint8_t*>(a.block) + m * a.ld_block * (B32 ? 4 : 2);
+  const uint8_t* h = static_cast<const uint8_t*>(a.residual) + m * a.ld_residual * (R32 ? 4 : 2);
+  const uint8_t* g = static_cast<const uint8_t*>(a.gate) + m * a.ld_gate * type_bytes(a.gate_type);
+  const bool g_early = a.gate && (a.gate_type == WR_F32) == W32;   // else (rare) it is loaded when it is used
+  const uint8_t* pw = static_cast<const uint8_t*>(a.post_weight);
+  const uint8_t* nw = static_cast<const uint8_t*>(a.norm_weight);
+  // everything the row needs before its last reduction is loaded at once; the last weights while that runs
+  Raw8<B32> rb[VPT];
+  Raw8<R32> rh[VPT];
+  Raw8<W32> rp[VPT], rg[VPT], rn[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (b) rb[i] = load8<VEC>(b, a.block_type, i, T, t, D);
-    if (h) rh[i] = load8<VEC>(h, a.residual_type, i, T, t, D);
-    if (kEarly && pw) rp[i] = load8<VEC>(pw, a.weight_type, i, T, t, D);
-    if (kEarly && g) rg[i] = load8<VEC>(g, a.gate_type, i, T, t, D);
-    if (kEarly && nw) rn[i] = load8<VEC>(nw, a.weight_type, i, T, t, D);
+    if (a.block) rb[i] = load8<B32, VEC>(b, i, T, t, D);
+    if (a.residual) rh[i] = load8<R32, VEC>(h, i, T, t, D);
+    if (g_early) rg[i] = load8<W32, VEC>(g, i, T, t, D);
+    if (pw) rp[i] = load8<W32, VEC>(pw, i, T, t, D);
   }
+  const f32x2 offset = splat2(a.weight_offset), rs = splat2(a.residual_scale);
+  auto scale8 = [&](Vec8& x, float r, const uint8_t* weight, const Raw8<W32>& rw) {
+    const f32x2 rr = splat2(r);
+    if (weight) {
+      const Vec8 w = to_float8(rw, a.weight_type);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.p[j] = mul2(mul2(x.p[j], rr), add2(w.p[j], offset));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.p[j] = mul2(x.p[j], rr);
+    }
+  };
+  // elements past the row are zero in every operand and stay so
+  Vec8 v[VPT];   // the block's output, then h'
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (b) to_float8(rb[i], a.block_type, v[i]);
+    if (a.block) v[i] = to_float8(rb[i], a.block_type);
     else
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) v[i].p[j] = splat2(0.f);
   }
   if (a.post_norm) {
-    float ss = 0.f;
+    f32x2 ss = splat2(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    const float r = 1.f / sqrtf(row_sum(ss, buf_post) * inv_d + a.eps);
+      for (int j = 0; j < 4; ++j) ss = fma2(v[i].p[j], v[i].p[j], ss);
+    const float r = rsqrtf(row_sum(ss, buf_post) * na.inv_d + a.eps);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      float w[8];
-      if (pw) {
-        if (!kEarly) rp[i] = load8<VEC>(pw, a.weight_type, i, T, t, D);
-        to_float8(rp[i], a.weight_type, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * (w[j] + a.weight_offset);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= r;
-      }
-    }
+    for (int i = 0; i < VPT; ++i) scale8(v[i], r, pw, rp[i]);
   }
-  float ss = 0.f;
+  f32x2 ss = splat2(0.f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (g) {
-      float w[8];
-      if (!kEarly) rg[i] = load8<VEC>(g, a.gate_type, i, T, t, D);
-      to_float8(rg[i], a.gate_type, w);
+    if (a.gate) {
+      const Vec8 w = g_early ? to_float8(rg[i], a.gate_type) : load_float8<VEC>(g, a.gate_type, i, T, t, D);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= w[j];
+      for (int j = 0; j < 4; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
     }
-    if (h) {
-      float w[8];
-      to_float8(rh[i], a.residual_type, w);
+    if (a.residual) {
+      const Vec8 w = to_float8(rh[i], a.residual_type);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(a.residual_scale, w[j], v[i][j]);
+      for (int j = 0; j < 4; ++j) v[i].p[j] = fma2(rs, w.p[j], v[i].p[j]);
     }
-    if (a.residual_out)
-      store8<VEC>(static_cast<uint8_t*>(a.residual_out) + m * a.ld_residual_out * type_bytes(a.residual_type),
-                  a.residual_type, i, T, t, D, v[i]);
-    // elements past the row are zero times whatever was loaded there (zero): they add nothing
+    if (nw) rn[i] = load8<W32, VEC>(nw, i, T, t, D);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    for (int j = 0; j < 4; ++j) ss = fma2(v[i].p[j], v[i].p[j], ss);
+  }
+  if (a.residual_out) {
+    uint8_t* o = static_cast<uint8_t*>(a.residual_out) + m * a.ld_residual_out * (R32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) store8<VEC>(o, a.residual_type, i, T, t, D, v[i]);
   }
   if (!a.y) return;
-  const float r = 1.f / sqrtf(row_sum(ss, buf_norm) * inv_d + a.eps);
-  uint32_t amax = 0;
+  const float r = rsqrtf(row_sum(ss, buf_norm) * na.inv_d + a.eps);
+  uint8_t* y = static_cast<uint8_t*>(a.y) + m * a.ld_y * type_bytes(a.y_type);
+  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    if (nw) {
-      float w[8];
-      if (!kEarly) rn[i] = load8<VEC>(nw, a.weight_type, i, T, t, D);
-      to_float8(rn[i], a.weight_type, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * r * (w[j] + a.weight_offset);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= r;
-    }
-    if (a.y_type == WR_I8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (elem<VEC>(i, j, T, t) < D) amax = max(amax, abs_bits(v[i][j]));
-    } else {
-      store8<VEC>(static_cast<uint8_t*>(a.y) + m * a.ld_y * type_bytes(a.y_type), a.y_type, i, T, t, D, v[i]);
-    }
+    scale8(v[i], r, nw, rn[i]);
+    // (a row with r = infinity or NaN is NaN in all its elements; past its end 0 r is NaN too)
+    if (a.y_type == WR_I8) amax = max_abs8(amax, v[i]);
+    else store8<VEC>(y, a.y_type, i, T, t, D, v[i]);
   }
   if (a.y_type == WR_I8) {
     const RowCode c = row_code(row_max(amax, buf_max));
-    int8_t* q = static_cast<int8_t*>(a.y) + m * a.ld_y;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) store_codes8<VEC>(q, i, T, t, D, c, v[i]);
+    for (int i = 0; i < VPT; ++i) store_codes8<VEC>(reinterpret_cast<int8_t*>(y), i, T, t, D, c, v[i]);
     if (t == 0) a.y_scale[m] = c.scale;
   }
 }
@@ -398,24 +494,78 @@ inline bool rows_aligned(int64_t M, int64_t ld, int bytes) { return M == 1 || ld
 // Threads that hold a row of D elements, VPT vectors of 8 each.
 inline int row_threads(int64_t D, int vpt) { return (int)std::min<int64_t>(1024, ((D + 8 * vpt - 1) / (8 * vpt) + 31) / 32 * 32); }
 
+// Vectors a thread. Few rows: one, the shortest way through a row. Many: two, since a thread's work in the
+// reductions is the same for 16 elements as for 8 and instructions run out before bandwidth does, while
+// four leave too few warps to hide the loads (8192 rows of 2560, fp32 block, bf16 residual: 48.0, 37.5 and
+// 58.8 us with one, two and four; 500 rows: 5.0, 4.6 and 6.6). Four where two would make a CTA of more
+// than `most` threads: the quantizer holds less and gains from four earlier (2000 gated rows of 8192 bf16:
+// 15.4 against 18.8 us; the norm: 37.6 against 31.9).
+constexpr int64_t kManyRows = 2 * 148;
+inline int row_vpt(int64_t M, int64_t D, int most) {
+  const int64_t vecs = (D + 7) / 8;
+  return vecs > 2 * most ? 4 : vecs <= (M < kManyRows ? 512 : 32) ? 1 : 2;
+}
+// The launch: a CTA for each row, or, where a warp holds a row, four rows a CTA.
+struct RowGrid {
+  dim3 grid, block;
+  RowGrid(int64_t M, int T) {
+    const unsigned rows = T == 32 && M >= kManyRows ? 4 : 1;
+    grid = dim3((unsigned)((M + rows - 1) / rows));
+    block = dim3((unsigned)T, rows);
+  }
+};
+
+template <int VPT, int MAXT, bool VEC>
+void run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
+  const RowGrid d(a.M, row_threads(a.K, VPT > 0 ? VPT : 4));
+  if (a.type == WR_F32) {
+    if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, true, true><<<d.grid, d.block, 0, stream>>>(a);
+    else quantize_rows_kernel<VPT, MAXT, VEC, true, false><<<d.grid, d.block, 0, stream>>>(a);
+  } else {
+    if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, false, true><<<d.grid, d.block, 0, stream>>>(a);
+    else quantize_rows_kernel<VPT, MAXT, VEC, false, false><<<d.grid, d.block, 0, stream>>>(a);
+  }
+}
+template <bool VEC>
+void run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
+  const int vpt = row_vpt(a.M, a.K, 256);
+  if (a.K > 32768) run_quantize<0, 1024, VEC>(a, stream);
+  else if (a.K > 16384) run_quantize<4, 1024, VEC>(a, stream);
+  else if (vpt == 1) run_quantize<1, 512, VEC>(a, stream);
+  else if (vpt == 2) run_quantize<2, 512, VEC>(a, stream);
+  else run_quantize<4, 512, VEC>(a, stream);
+}
+
+template <int VPT, int MAXT, bool VEC, bool B32, bool R32>
+void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+  const RowGrid d(a.p.M, row_threads(a.p.D, VPT));
+  if (w32) residual_norm_kernel<VPT, MAXT, VEC, B32, R32, true><<<d.grid, d.block, 0, stream>>>(a);
+  else residual_norm_kernel<VPT, MAXT, VEC, B32, R32, false><<<d.grid, d.block, 0, stream>>>(a);
+}
+template <int VPT, int MAXT, bool VEC>
+void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+  const bool b32 = a.p.block_type == WR_F32, r32 = a.p.residual_type == WR_F32;
+  if (b32 && r32) run_norm<VPT, MAXT, VEC, true, true>(a, w32, stream);
+  else if (b32) run_norm<VPT, MAXT, VEC, true, false>(a, w32, stream);
+  else if (r32) run_norm<VPT, MAXT, VEC, false, true>(a, w32, stream);
+  else run_norm<VPT, MAXT, VEC, false, false>(a, w32, stream);
+}
+template <bool VEC>
+void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+  const int vpt = row_vpt(a.p.M, a.p.D, 512);
+  if (a.p.D > 16384) run_norm<4, 1024, VEC>(a, w32, stream);
+  else if (vpt == 1) run_norm<1, 512, VEC>(a, w32, stream);
+  else if (vpt == 2) run_norm<2, 512, VEC>(a, w32, stream);
+  else run_norm<4, 512, VEC>(a, w32, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_quantize_rows(const QuantRowsArgs& a, cudaStream_t stream) {
   const int es = type_bytes(a.type);
   const bool vec = rows_aligned(a.M, a.ldx, es) && (!a.gate || rows_aligned(a.M, a.ldg, es)) && (a.M == 1 || a.ldq % 8 == 0);
-  const unsigned grid = (unsigned)a.M;
-#define WR_QUANT(VPT, MAXT)                                                                                  \
-  do {                                                                                                       \
-    const int T = row_threads(a.K, VPT > 0 ? VPT : 4);                                                       \
-    if (vec) quantize_rows_kernel<VPT, MAXT, true><<<grid, T, 0, stream>>>(a);                               \
-    else quantize_rows_kernel<VPT, MAXT, false><<<grid, T, 0, stream>>>(a);                                  \
-  } while (0)
-  if (a.K <= 4096) WR_QUANT(1, 512);
-  else if (a.K <= 8192) WR_QUANT(2, 512);
-  else if (a.K <= 16384) WR_QUANT(4, 512);
-  else if (a.K <= 32768) WR_QUANT(4, 1024);
-  else WR_QUANT(0, 1024);
-#undef WR_QUANT
+  if (vec) run_quantize<true>(a, stream);
+  else run_quantize<false>(a, stream);
   return cudaGetLastError();
 }
 
@@ -425,18 +575,10 @@ cudaError_t launch_residual_norm(const wr_residual_norm_args& a, cudaStream_t st
                    (!a.residual_out || rows_aligned(a.M, a.ld_residual_out, type_bytes(a.residual_type))) &&
                    (!a.gate || rows_aligned(a.M, a.ld_gate, type_bytes(a.gate_type))) &&
                    (!a.y || (a.y_type == WR_I8 ? a.M == 1 || a.ld_y % 8 == 0 : rows_aligned(a.M, a.ld_y, type_bytes(a.y_type))));
-  const unsigned grid = (unsigned)a.M;
-#define WR_NORM(VPT, MAXT)                                                                                   \
-  do {                                                                                                       \
-    const int T = row_threads(a.D, VPT);                                                                     \
-    if (vec) residual_norm_kernel<VPT, MAXT, true><<<grid, T, 0, stream>>>(a);                               \
-    else residual_norm_kernel<VPT, MAXT, false><<<grid, T, 0, stream>>>(a);                                  \
-  } while (0)
-  if (a.D <= 4096) WR_NORM(1, 512);
-  else if (a.D <= 8192) WR_NORM(2, 512);
-  else if (a.D <= 16384) WR_NORM(4, 512);
-  else WR_NORM(4, 1024);
-#undef WR_NORM
+  NormArgs na{a, (float)(1.0 / (double)a.D)};
+  const bool w32 = a.post_weight || a.norm_weight ? a.weight_type == WR_F32 : a.gate_type == WR_F32;
+  if (vec) run_norm<true>(na, w32, stream);
+  else run_norm<false>(na, w32, stream);
   return cudaGetLastError();
 }
 

@@ -114,8 +114,8 @@ def exported_symbols():
 
 
 def _load():
-    if not os.path.exists(LIB_PATH):
-        raise ImportError(f"libwr.so not found at {LIB_PATH}; build it with "
+    if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")):
+        raise ImportError(f"libwr.so or _marshal.so not found beside {LIB_PATH}; build them with "
                           "`python bit_weight_only_wr_b200/build.py` (nvcc, sm_100a)")
     lib = ctypes.CDLL(LIB_PATH)
     for name, (res, args) in _SIGNATURES.items():
@@ -370,80 +370,19 @@ def wr_quantize_pack(bits: int, N: int, K: int, w, packed, scales, stream=None) 
                                                      _stream(stream)))
 
 
-def _torch_calls():
-    """(current device, raw current stream of a device) of torch, looked up once: the calls below make
-    them for every launch, and torch.cuda.current_stream() alone takes longer than a small kernel."""
-    global _torch_calls
-    import torch
-    torch.cuda.init()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    found = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
-             raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
-    _torch_calls = lambda: found  # noqa: E731
-    return found
-
-
-def _device_ptrs(operands, stream):
-    """Addresses of device operands (tensors, addresses or None), then the stream's. A tensor has to be on
-    the current CUDA device: the library launches there."""
-    dev = raw = None
-    out = []
-    for t in operands:
-        if t is None or type(t) is int:
-            out.append(t)
-            continue
-        if dev is None:
-            if not t.is_cuda:
-                raise ValueError("expected a CUDA tensor, got one on the host")
-            current, raw = _torch_calls()
-            dev = current()
-        if t.get_device() != dev:
-            raise ValueError(f"tensor on device {t.device}, but the current device is cuda:{dev}")
-        out.append(t.data_ptr())
-    if stream is None:
-        if raw is None:
-            current, raw = _torch_calls()
-            dev = current()
-        out.append(raw(dev))
-    else:
-        out.append(stream if type(stream) is int else stream.cuda_stream)
-    return out
-
-
-def wr_quantize_rows(type: int, M: int, K: int, x, ldx: int, q, ldq: int, scale, gate=None, ldg: int = 0,
-                     stream=None) -> None:
-    """Rows of x (or of silu(gate) * x) -> int8 codes q and one fp32 scale per row (device)."""
-    x, gate, q, scale, stream = _device_ptrs((x, gate, q, scale), stream)
-    _check("wr_quantize_rows", _lib.wr_quantize_rows(type, M, K, x, ldx, gate, ldg, q, ldq, scale, stream))
-
-
 def wr_gemm_i8_workspace_bytes(M: int, N: int, K: int) -> int:
     return _lib.wr_gemm_i8_workspace_bytes(M, N, K)
 
 
-def wr_gemm_i8(M: int, N: int, K: int, x, ldx: int, x_scale, w, ldw: int, w_scale, y_type: int, y, ldy: int, workspace,
-               workspace_bytes: int, bias=None, stream=None) -> None:
-    """y = (x w^T) * x_scale[:, None] * w_scale (+ bias) from int8 tokens and int8 output channels."""
-    x, x_scale, w, w_scale, bias, y, workspace, stream = _device_ptrs((x, x_scale, w, w_scale, bias, y, workspace), stream)
-    _check("wr_gemm_i8", _lib.wr_gemm_i8(M, N, K, x, ldx, x_scale, w, ldw, w_scale, bias, y_type, y, ldy, workspace,
-                                         workspace_bytes, stream))
+# The calls of the 8-bit token path take about as long on the GPU as ctypes takes to convert their
+# arguments; an extension module does that instead (csrc/python/marshal.cpp; the signatures are in its
+# docstrings). Tensors have to be on the current CUDA device.
+from . import _marshal  # noqa: E402
 
-
-def wr_residual_norm(M: int, D: int, *, block=None, ld_block: int = 0, block_type: int = WR_F32, residual=None,
-                     ld_residual: int = 0, residual_out=None, ld_residual_out: int = 0, residual_type: int = WR_F32,
-                     gate=None, ld_gate: int = 0, gate_type: int = WR_F32, post_weight=None, norm_weight=None,
-                     weight_type: int = WR_F32, weight_offset: float = 0.0, post_norm: bool | None = None, y=None,
-                     ld_y: int = 0, y_type: int = WR_F32, y_scale=None, residual_scale: float = 1.0, eps: float = 1e-6,
-                     stream=None) -> None:
-    """h' = residual_scale * residual + gate * post(block) and y = norm(h'), in one pass (wr_residual_norm
-    of include/wr.h). post_norm: whether the block's output is normed first; by default, whether
-    post_weight is given."""
-    if post_norm is None:
-        post_norm = post_weight is not None
-    *ptrs, stream = _device_ptrs((block, residual, gate, post_weight, norm_weight, residual_out, y, y_scale), stream)
-    a = WrResidualNormArgs(M, D, *ptrs, ld_block, ld_residual, ld_gate, ld_residual_out, ld_y, block_type, residual_type,
-                           gate_type, weight_type, y_type, post_norm, eps, residual_scale, weight_offset, 0)
-    _check("wr_residual_norm", _lib.wr_residual_norm(a, stream))
+_marshal.set_error(WrError)
+wr_quantize_rows = _marshal.wr_quantize_rows
+wr_gemm_i8 = _marshal.wr_gemm_i8
+wr_residual_norm = _marshal.wr_residual_norm
 
 
 def wr_selftest_wait_timeout(stream=None) -> None:

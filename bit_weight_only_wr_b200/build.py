@@ -1,9 +1,11 @@
-"""Build libwr.so in-tree for sm_100a (nvcc for the .cu files, g++ for host C++)."""
+"""Build libwr.so in-tree for sm_100a (nvcc for the .cu files, g++ for host C++), and beside it the
+Python extension module that marshals arguments for part of it."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwr.so")
+MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -62,6 +66,9 @@ def build(verbose: bool = False, extra_nvcc: list[str] | None = None) -> str:
     objs = [os.path.join(BUILD, f + ".o") for f in cu + cpp]
     if jobs or _newer(objs, LIB):
         run([NVCC] + ARCH + ["-shared", "-o", LIB] + objs + ["-Xcompiler", "-fopenmp", "-lgomp"])
+    if _newer([MARSHAL_SRC, LIB, os.path.join(INCLUDE, "wr.h")], MARSHAL):
+        run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+             MARSHAL_SRC, "-o", MARSHAL, "-L", PKG, "-l:libwr.so", "-Wl,-rpath,$ORIGIN"])
     return LIB
 
 

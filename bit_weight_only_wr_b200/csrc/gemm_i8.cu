@@ -121,13 +121,15 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 // swizzle, zeros behind the ends of K, M and N). Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 are the
 // epilogue (TMEM lanes 32 (warp % 4) ..). Every wait is bounded.
 //
-// Two forms (plan_gemm_i8 chooses by the time it expects of each):
-//   split  a cluster of `split` CTAs shares a tile, each with its part of K; they leave their int32 sums
-//          in shared memory and each finishes its part of the tokens from all of them. Two CTAs fit an SM.
-//   pair   persistent CTA pairs (cta_group::2): a pair loads each operand once for 256 x tn outputs, and
-//          the epilogue of a tile overlaps the products of the next (two accumulators).
+// CTA pairs (cta_group::2) load each operand once for 256 x tn outputs. Two forms (plan_gemm_i8 chooses
+// by the time it expects of each):
+//   split       a cluster of `split` CTAs, or pairs, shares a tile, each with its part of K; they leave their
+//               int32 sums in shared memory and each finishes its part of the tokens from all of them.
+//               Two CTAs fit an SM.
+//   persistent  pairs take whole tiles in turn; the epilogue of a tile overlaps the products of the next
+//               (two accumulators).
 constexpr int kGemmThreads = 192;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 12;
 
 struct GemmBars {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
@@ -178,20 +180,6 @@ __device__ __forceinline__ void drain(GemmBars& bars, const Ring& r, int stages)
   }
 }
 
-// x_scale of 16 tokens (`left` of them real; the address is 64-byte aligned).
-__device__ __forceinline__ void load_scales16(const float* xs, int left, float v[16]) {
-  if (left >= 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(xs) + i);
-      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < left ? __ldg(xs + i) : 0.f;
-  }
-}
-
 // Writes this thread's channel of 16 tokens from token m on (`left` of them real): v plus the bias. A
 // warp holds 32 neighbouring channels, so a token's store is 128 contiguous bytes of fp32. For a
 // 16-bit y neighbouring lanes exchange halves, so that even lanes store pairs of channels of the even
@@ -237,67 +225,178 @@ __device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, in
     if (i < left) y[i * a.ldy] = (uint16_t)h[i];
 }
 
-// 16 tokens of one channel from their sums.
-__device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16], int m, int left, int ch, int lane, float ws, float bias) {
-  float xs[16], v[16];
-  load_scales16(a.x_scale + m, left, xs);
+// 16 tokens of one channel from their sums. xs: their scales (shared memory, readable past `left`).
+__device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16], const float* xs, int m, int left, int ch, int lane, float ws,
+                                         float bias) {
+  float v[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = (float)sum[i] * xs[i] * ws;
   store16(a, m, left, ch, lane, v, bias);
 }
 
-// ---- split form: cluster rank r of tile t takes K blocks [r kb / split, (r + 1) kb / split)
+// The scales of a tile's tokens, to shared memory, by the 128 threads of the epilogue.
+__device__ __forceinline__ void stage_scales(float* to, const float* x_scale, int cols, int tn, int t) {
+  for (int i = t; i < tn; i += 128) to[i] = i < cols ? __ldg(x_scale + i) : 0.f;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The end of a split tile: all parts' sums lie in shared memory as [token][128 channels]. This part's tokens are
+// part, part + split, ...; a warp takes every sixth of them (four at a time, for loads in flight), a lane
+// four neighbouring channels.
+template <int CG>
+__device__ __forceinline__ void exchange(const GemmParams& p, const uint8_t* ring, const float* xs, int part, int half, int n0, int m0,
+                                         int cols, int warp, int lane) {
+  constexpr int kWarps = kGemmThreads / 32, kBatch = 4;
+  const int ch = n0 + 4 * lane, real = min(4, p.a.N - ch);   // channels of this lane that exist
+  float ws[4], bias[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    ws[e] = e < real ? __ldg(p.a.w_scale + ch + e) : 0.f;
+    bias[e] = p.a.bias && e < real ? __ldg(p.a.bias + ch + e) : 0.f;
+  }
+  const bool whole = real == 4 && (p.a.ldy & 3) == 0;        // four channels in one store
+  for (int c0 = part + p.split * warp; c0 < cols; c0 += p.split * kWarps * kBatch) {
+    int sum[kBatch][4] = {};
+#pragma unroll 2
+    for (int c = 0; c < p.split; ++c) {
+      const uint32_t src = cluster_addr(ring, c * CG + half) + 16 * lane;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int tok = c0 + i * p.split * kWarps;
+        if (tok < cols) {
+          const int4 v = ld_cluster_v4(src + tok * 512);
+          sum[i][0] += v.x; sum[i][1] += v.y; sum[i][2] += v.z; sum[i][3] += v.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int tok = c0 + i * p.split * kWarps;
+      if (tok >= cols) break;
+      const float x = xs[tok];
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = (float)sum[i][e] * x * ws[e];
+        if (p.a.bias) v[e] += bias[e];
+      }
+      const int64_t at = (int64_t)(m0 + tok) * p.a.ldy + ch;
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < real) store_y(p.a.y, p.a.y_type, at + e, v[e]);
+      } else if (p.a.y_type == WR_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        uint2 h;
+        if (p.a.y_type == WR_BF16) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+          h = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+          const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
+          h = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.y) + at) = h;
+      }
+    }
+  }
+}
+
+// ---- split form: part r of tile t takes K blocks [r kb / split, (r + 1) kb / split). A part is a CTA, or
+// with PAIR two neighbouring CTAs of the cluster (256 channels a tile).
+template <bool PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 2)
     gemm_i8_split_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ GemmBars bars;
+  constexpr int CG = PAIR ? 2 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  const int size = CG * p.split, rank = blockIdx.x % size, tile = blockIdx.x / size;
+  const int part = rank / CG, half = rank % CG, leader = rank - half;
+  const uint16_t mask = (uint16_t)(3 << leader);
   const int rg = tile / p.mt, mt = tile - rg * p.mt;
-  const int n0 = rg * 128, m0 = mt * p.tn;
-  const int k0 = rank * p.kb / p.split, k1 = (rank + 1) * p.kb / p.split;
-  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)p.tn * 128;
+  const int n0 = (rg * CG + half) * 128, m0 = mt * p.tn;
+  const int k0 = part * p.kb / p.split, k1 = (part + 1) * p.kb / p.split;
+  const int b_rows = p.tn / CG;                       // tokens that this CTA loads
+  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)b_rows * 128;
   volatile int* abort_flag = &bars.abort_flag;
-  init_bars(bars, p.stages, 4);
-  if (warp == 1) tmem_alloc(&bars.tmem_base, p.tmem_cols);
-  fence_before_sync();
-  __syncthreads();
-  fence_after_sync();
-  const uint32_t tmem = bars.tmem_base;
   const int q = warp & 3, row = 32 * q + lane, ch = n0 + row;
   const int cols = min(p.tn, p.a.M - m0);   // tokens of this tile
   float ws = 0.f, bias = 0.f;
+  __shared__ float xs[256];
+
+  // A CTA of its own fills the ring before it meets the other warps; a pair's copies complete on the
+  // leader's barriers, which have to be there first.
+  int k_next = k0;
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tensormap(&wmap);
+      prefetch_tensormap(&xmap);
+    }
+    init_bars(bars, p.stages, 4);
+    if (!PAIR && lane == 0) {
+      for (int i = 0; i < p.stages && k_next < k1; ++i, ++k_next) {
+        mbar_arrive_expect_tx(&bars.full[i], stage_bytes);
+        tma_load_2d(ring + i * stage_bytes, &wmap, k_next * 128, n0, &bars.full[i]);
+        tma_load_2d(ring + i * stage_bytes + a_bytes, &xmap, k_next * 128, m0, &bars.full[i]);
+      }
+    }
+  } else if (warp == 1) {
+    if (PAIR) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
+    else tmem_alloc(&bars.tmem_base, p.tmem_cols);
+  } else {
+    stage_scales(xs, p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
+    if (ch < p.a.N) {
+      ws = __ldg(p.a.w_scale + ch);
+      if (p.a.bias) bias = __ldg(p.a.bias + ch);
+    }
+  }
+  fence_before_sync();
+  if (PAIR) cluster_sync();
+  else __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = bars.tmem_base;
 
   if (warp == 0) {
     if (lane == 0) {
       Ring r;
       bool ok = true;
       for (int k = k0; k < k1; ++k, r.next(p.stages)) {
+        if (k < k_next) continue;
         if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 501))) break;
         uint8_t* st = ring + r.s * stage_bytes;
-        mbar_arrive_expect_tx(&bars.full[r.s], stage_bytes);
-        tma_load_2d(st, &wmap, k * 128, n0, &bars.full[r.s]);
-        tma_load_2d(st + a_bytes, &xmap, k * 128, m0, &bars.full[r.s]);
+        if (PAIR) {
+          // both CTAs' copies complete on the leader's barrier
+          if (half == 0) mbar_arrive_expect_tx(&bars.full[r.s], 2 * stage_bytes);
+          const uint32_t bar = cluster_addr(&bars.full[r.s], leader);
+          tma_load_2d_pair(st, &wmap, k * 128, n0, bar);
+          tma_load_2d_pair(st + a_bytes, &xmap, k * 128, m0 + half * b_rows, bar);
+        } else {
+          mbar_arrive_expect_tx(&bars.full[r.s], stage_bytes);
+          tma_load_2d(st, &wmap, k * 128, n0, &bars.full[r.s]);
+          tma_load_2d(st + a_bytes, &xmap, k * 128, m0, &bars.full[r.s]);
+        }
       }
-      if (!ok) drain(bars, r, p.stages);
+      if (!ok && half == 0) drain(bars, r, p.stages);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_i8s(128, p.tn);
-    Ring r;
-    bool ok = true;
-    for (int k = k0; k < k1; ++k, r.next(p.stages)) {
-      if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 503))) break;
-      fence_after_sync();
-      const uint8_t* st = ring + r.s * stage_bytes;
-      mma4_i8_ss_commit_elect<false>(tmem, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != k0, &bars.empty[r.s]);
+    if (half == 0) {   // a pair's leader issues for both CTAs
+      const uint32_t idesc = idesc_i8s(128 * CG, p.tn);
+      Ring r;
+      bool ok = true;
+      for (int k = k0; k < k1; ++k, r.next(p.stages)) {
+        if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 503))) break;
+        fence_after_sync();
+        const uint8_t* st = ring + r.s * stage_bytes;
+        mma4_i8_ss_commit_elect<PAIR>(tmem, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != k0, &bars.empty[r.s], mask);
+      }
+      if (ok) {
+        if (PAIR) mma_commit_pair_elect(&bars.acc_full[0], mask);
+        else mma_commit_elect(&bars.acc_full[0]);
+      }
     }
-    if (ok) mma_commit_elect(&bars.acc_full[0]);
   } else {
-    if (ch < p.a.N) {
-      ws = __ldg(p.a.w_scale + ch);
-      if (p.a.bias) bias = __ldg(p.a.bias + ch);
-    }
     if (mbar_wait(&bars.acc_full[0], 0, abort_flag, p.err, 504)) {
       fence_after_sync();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
@@ -310,7 +409,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
         if (p.split == 1) {
-          finish16(p.a, sum, m0 + c0, cols - c0, ch, lane, ws, bias);
+          finish16(p.a, sum, xs + c0, m0 + c0, cols - c0, ch, lane, ws, bias);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[(c0 + i) * 128] = sum[i];
@@ -321,32 +420,21 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   }
   if (p.split > 1) {
     cluster_sync();   // all parts are in shared memory
-    if (warp >= 2 && !*abort_flag) {
-      // groups of 16 tokens (one group at most 16): this CTA's are rank, rank + split, ... in steps of `g`
-      const int g = min(16, (cols + p.split - 1) / p.split);
-      for (int c0 = rank * g; c0 < cols; c0 += p.split * g) {
-        int sum[16] = {};
-        const int left = min(g, cols - c0);
-        for (int c = 0; c < p.split; ++c) {
-          const uint32_t src = cluster_addr(ring, c) + (uint32_t)(c0 * 128 + row) * 4;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < left) sum[i] += ld_cluster(src + i * 512);
-        }
-        finish16(p.a, sum, m0 + c0, left, ch, lane, ws, bias);
-      }
-    }
-    cluster_sync();   // nobody leaves while its shared memory is read
-  } else {
-    __syncthreads();
+    if (!*abort_flag) exchange<CG>(p, ring, xs, part, half, n0, m0, cols, warp, lane);
   }
+  fence_before_sync();
+  if (size > 1) cluster_sync();   // nobody leaves while its shared memory (or tensor memory) is in use
+  else __syncthreads();
   fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
+  if (warp == 1) {
+    if (PAIR) tmem_dealloc_pair(tmem, p.tmem_cols);
+    else tmem_dealloc(tmem, p.tmem_cols);
+  }
 }
 
-// ---- pair form
+// ---- persistent form
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    gemm_i8_pair_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+    gemm_i8_persistent_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ GemmBars bars;
@@ -356,7 +444,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int b_rows = p.tn / 2;                       // tokens that this CTA loads
   const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)b_rows * 128;
   volatile int* abort_flag = &bars.abort_flag;
-  init_bars(bars, p.stages, 8);
+  __shared__ float xs[2][256];
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tensormap(&wmap);
+      prefetch_tensormap(&xmap);
+    }
+    init_bars(bars, p.stages, 8);
+  }
   if (warp == 1) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
   fence_before_sync();
   cluster_sync();
@@ -397,9 +492,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           fence_after_sync();
           const uint8_t* st = ring + r.s * stage_bytes;
           mma4_i8_ss_commit_elect<true>(tmem + d * p.tn, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != 0,
-                                        &bars.empty[r.s]);
+                                        &bars.empty[r.s], 3);
         }
-        if (ok) mma_commit_pair_elect(&bars.acc_full[d]);
+        if (ok) mma_commit_pair_elect(&bars.acc_full[d], 3);
       }
     }
   } else {
@@ -412,6 +507,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int cols = min(p.tn, p.a.M - m0);         // tokens of this tile
       const float ws = ch < p.a.N ? __ldg(p.a.w_scale + ch) : 0.f;
       const float bias = p.a.bias && ch < p.a.N ? __ldg(p.a.bias + ch) : 0.f;
+      stage_scales(xs[d], p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
+      epilogue_sync();   // (xs[d] was last read two tiles ago, before the other one's barrier)
       if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
       fence_after_sync();
       const uint32_t acc = tmem + d * p.tn + ((uint32_t)(32 * q) << 16);
@@ -422,7 +519,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
-        finish16(p.a, sum, m0 + c0, cols - c0, ch, lane, ws, bias);
+        finish16(p.a, sum, xs[d] + c0, m0 + c0, cols - c0, ch, lane, ws, bias);
       }
       fence_before_sync();
       __syncwarp();
@@ -436,7 +533,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 }
 
 constexpr int kSMs = 148;
-constexpr int kSplitRing = 96 * 1024, kPairRing = 208 * 1024;   // two split CTAs, or one of a pair, fill an SM
+constexpr int kRing = 96 * 1024, kDeepRing = 208 * 1024;   // of a CTA that shares its SM with another, and of one that does not
 
 // Shared memory limits are set once per device and kernel.
 template <typename Kernel>
@@ -466,39 +563,29 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
   constexpr double kL2Bytes = 48;
   const int64_t mt0 = (M + 255) / 256, mt1 = std::min<int64_t>((M + 15) / 16, mt0 + 7);
   for (int64_t mt = mt0; mt <= mt1; ++mt) {
-    {
-      const int tn = (int)(((M + mt - 1) / mt + 15) / 16 * 16);
-      const int64_t tiles = (M + tn - 1) / tn * ((N + 127) / 128);
+    for (int pair = 0; pair < (N > 128 && M > 16 ? 2 : 1); ++pair) {
+      const int cg = 1 + pair, step = 16 * cg;
+      const int tn = (int)(((M + mt - 1) / mt + step - 1) / step * step);
+      const int64_t mtiles = (M + tn - 1) / tn, tiles = mtiles * ((N + 128 * cg - 1) / (128 * cg));
       if (tiles > (1 << 26)) return false;
-      const double block = std::max(2.0 * tn, (16384 + 128.0 * tn) / kL2Bytes);
-      for (int s = 1; s <= std::min(8, kb); ++s) {
-        const int64_t rounds = (tiles * s + kSMs - 1) / kSMs;
-        const double t = rounds * ((kb + s - 1) / s) * block + (rounds + 1) / 2 * (1500 + 8.0 * tn) + (s > 1 ? 800 + 4.0 * tn : 0);
-        if (p->tn == 0 || t < best) {
-          best = t;
-          p->pair = 0;
-          p->tn = tn;
-          p->mt = (int)((M + tn - 1) / tn);
-          p->tiles = (int)tiles;
-          p->split = s;
-          p->workers = (int)tiles;
-        }
-      }
-    }
-    if (N > 128 && M > 32) {
-      const int tn = (int)(((M + mt - 1) / mt + 31) / 32 * 32);
-      const int64_t tiles = (M + tn - 1) / tn * ((N + 255) / 256);
-      const double block = std::max(2.0 * tn, (16384 + 64.0 * tn) / kL2Bytes);
-      const int64_t rounds = (tiles + kSMs / 2 - 1) / (kSMs / 2);
-      const double t = rounds * std::max((double)kb * block, 500 + 12.0 * tn) + 2000 + 12.0 * tn;
-      if (t < best) {
+      const double block = std::max(2.0 * tn, (16384 + 128.0 * tn / cg) / kL2Bytes);
+      auto offer = [&](int persistent, int split, double t) {
+        if (p->tn != 0 && t >= best) return;
         best = t;
-        p->pair = 1;
+        p->pair = pair;
+        p->persistent = persistent;
         p->tn = tn;
-        p->mt = (int)((M + tn - 1) / tn);
+        p->mt = (int)mtiles;
         p->tiles = (int)tiles;
-        p->split = 1;
-        p->workers = (int)std::min<int64_t>(tiles, kSMs / 2);
+        p->split = split;
+      };
+      for (int s = 1; s <= std::min(8 / cg, kb); ++s) {
+        const int64_t rounds = (tiles * s * cg + kSMs - 1) / kSMs;
+        offer(0, s, rounds * ((kb + s - 1) / s) * block + (rounds + 1) / 2 * (1500 + 8.0 * tn) + (s > 1 ? 800 + 4.0 * tn : 0));
+      }
+      if (pair) {
+        const int64_t rounds = (tiles + kSMs / 2 - 1) / (kSMs / 2);
+        offer(1, 1, rounds * std::max((double)kb * block, 500 + 12.0 * tn) + 2000 + 12.0 * tn);
       }
     }
   }
@@ -506,7 +593,7 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
 }
 
 cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, cudaStream_t stream) {
-  const int cg = pl.pair ? 2 : 1;
+  const int cg = 1 + pl.pair;
   GemmParams p{};
   p.a = a;
   p.tn = pl.tn;
@@ -515,32 +602,35 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   p.tiles = pl.tiles;
   p.split = pl.split;
   const int stage = 128 * 128 + pl.tn / cg * 128;
-  p.stages = std::min(kMaxStages, (pl.pair ? kPairRing : kSplitRing) / stage);
+  const int cluster = pl.persistent ? 2 : cg * pl.split;
+  const int64_t ctas = (int64_t)(pl.persistent ? std::min(pl.tiles, kSMs / 2) : pl.tiles) * cluster;
+  // a CTA that has its SM for itself takes the deeper ring
+  const int room = pl.persistent || ctas <= kSMs ? kDeepRing : kRing;
+  p.stages = std::min({kMaxStages, room / stage, std::max(1, (pl.kb + pl.split - 1) / pl.split * (pl.persistent ? kMaxStages : 1))});
   p.tmem_cols = 32;
-  while (p.tmem_cols < cg * pl.tn) p.tmem_cols *= 2;   // two accumulators in the pair form
+  while (p.tmem_cols < (pl.persistent ? 2 : 1) * pl.tn) p.tmem_cols *= 2;   // two accumulators in the persistent form
   p.err = err;
   CUtensorMap wmap, xmap;
   if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg))
     return cudaErrorInvalidValue;
-  static bool split_done[64], pair_done[64];
-  cudaError_t e = pl.pair ? allow_smem(gemm_i8_pair_kernel, kPairRing + 1024, pair_done)
-                          : allow_smem(gemm_i8_split_kernel, 128 * 1024 + 1024, split_done);
+  const auto kern = pl.persistent ? gemm_i8_persistent_kernel : pl.pair ? gemm_i8_split_kernel<true> : gemm_i8_split_kernel<false>;
+  static bool done[3][64];
+  const cudaError_t e = allow_smem(kern, kDeepRing + 1024, done[pl.persistent ? 2 : pl.pair]);
   if (e != cudaSuccess) return e;
   // the ring, or the sums that replace it at the end of a split tile
-  const int ring = pl.pair ? kPairRing : std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
+  const int ring = std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pl.workers * (pl.pair ? 2 : pl.split)));
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = (size_t)ring + 1024;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = pl.pair ? 2 : (unsigned)pl.split;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return pl.pair ? cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel, p, wmap, xmap)
-                 : cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel, p, wmap, xmap);
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p, wmap, xmap);
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {

@@ -38,13 +38,13 @@ struct GemmI8Args {
 };
 // The work of one call on the tensor cores, planned on the host (see gemm_i8.cu).
 struct GemmI8Plan {
-  int pair;        // 1: CTA pairs (256 channels a tile), 0: clusters of `split` CTAs (128)
+  int pair;        // 1: CTA pairs (256 channels a tile), 0: single CTAs (128)
+  int persistent;  // 1: pairs that take tiles in turn, 0: a cluster for each tile
   int tn;          // tokens a tile
   int mt;          // token tiles
   int kb;          // 128-byte blocks of K
-  int split;       // CTAs that share a tile's K
+  int split;       // parts of a tile's K
   int tiles;
-  int workers;     // pairs, or clusters, of the launch
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
 // Tokens up to which the product runs on dp4a, without a workspace.

@@ -259,10 +259,11 @@ __host__ __device__ constexpr uint32_t idesc_i8s(int m, int n) {
 // The 4 K steps of 32 of one 128-byte stage, both operands in shared memory, and the commit that
 // frees the stage: one election for the five instructions (see mma8_i8_commit_elect). The first step
 // overwrites D unless `accumulate`. PAIR: the CTA pair's MMA (256 rows, each CTA holds 128 of A and
-// half of B at the same shared-memory addresses); the commit arrives in both CTAs.
+// half of B at the same shared-memory addresses); the commit arrives in the CTAs of the cluster that
+// `mask` names, both of the pair.
 template <bool PAIR>
 __device__ __forceinline__ void mma4_i8_ss_commit_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                        uint32_t accumulate, uint64_t* bar) {
+                                                        uint32_t accumulate, uint64_t* bar, uint16_t mask = 0) {
   if constexpr (PAIR) {
     asm volatile(
         "{\n .reg .pred e, p;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
@@ -272,7 +273,7 @@ __device__ __forceinline__ void mma4_i8_ss_commit_elect(uint32_t d_tmem, uint64_
         " @e tcgen05.mma.cta_group::2.kind::i8 [%0], %9, %10, %3, 1;\n"
         " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12;\n}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "l"(a_desc + 2), "l"(b_desc + 2), "l"(a_desc + 4), "l"(b_desc + 4),
-        "l"(a_desc + 6), "l"(b_desc + 6), "r"(smem_u32(bar)), "h"((uint16_t)3)
+        "l"(a_desc + 6), "l"(b_desc + 6), "r"(smem_u32(bar)), "h"(mask)
         : "memory");
   } else {
     asm volatile(
@@ -301,9 +302,10 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+// 16 bytes of another CTA's shared memory (not volatile: several may be in flight; cluster_sync orders them).
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+  int4 v;
+  asm("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 // All threads of the cluster's CTAs (the aligned form: each warp arrives as one).
@@ -322,11 +324,11 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_pair_elect(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
       " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {

@@ -28,25 +28,29 @@ __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v) 
   else static_cast<__half*>(y)[at] = __float2half_rn(v);
 }
 
-// ---------------------------------------------------------------- few tokens: dp4a, one pass over w
+// ---------------------------------------------------------------- one or two tokens: dp4a, one pass over w
 
-// The 16 bytes at k of a row of K bytes, zero behind its end (nothing behind the row is read).
-template <bool STREAM>
-__device__ __forceinline__ uint4 row_chunk(const int8_t* row, int k, int K) {
-  if (k + 16 <= K) {
-    if (STREAM) return ld_stream_v4(row + k);
-    return __ldg(reinterpret_cast<const uint4*>(row + k));
-  }
-  uint32_t w[4] = {0, 0, 0, 0};
-  for (int i = 0; i < 16; ++i) {
-    if (k + i < K) {
-      const uint32_t b = (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
-      if (i < 4) w[0] |= b;
-      else if (i < 8) w[1] |= b;
-      else if (i < 12) w[2] |= b;
-      else w[3] |= b;
-    }
-  }
+// 16 bytes, or zeros (no load) where !in.
+__device__ __forceinline__ uint4 chunk_if(const int8_t* p, bool in) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+      : "l"(p), "r"((int)in));
+  return v;
+}
+// The last `n` < 16 bytes of a row (p 16-byte aligned), then zeros: whole words, then single bytes.
+__device__ __forceinline__ uint4 row_end(const int8_t* p, int n) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = 4 * i + 4 <= n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+  uint32_t rest = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if ((n & ~3) + i < n) rest |= (uint32_t)(uint8_t)__ldg(p + (n & ~3) + i) << (8 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i == n / 4) w[i] = rest;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -57,59 +61,69 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
   return __dp4a((int)a.w, (int)b.w, acc);
 }
 
-// A warp owns R rows of w and MT tokens and reads the rows once, 512 bytes of each a step; x stays in
-// L1. grid.y covers the tokens in steps of MT.
-template <int R, int MT>
-__global__ void __launch_bounds__(128) gemv_i8_kernel(const GemmI8Args a) {
-  const int lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * R, m0 = blockIdx.y * MT;
-  if (n0 >= a.N) return;
-  const int8_t *w[R], *x[MT];
+// `share` warps (1, 2 or 4) of a CTA share a row of w and read it once, 512 bytes a warp and step with eight
+// steps in flight; x comes from L1. Memory latency is what a matrix of this size is bound by, so share is
+// what lets a warp have all of its bytes on their way at once (up to K = 16384).
+constexpr int kGemvThreads = 128;
+template <int MT>
+__global__ void __launch_bounds__(kGemvThreads) gemv_i8_kernel(const GemmI8Args a, const int share) {
+  __shared__ int parts[kGemvThreads / 32][MT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = blockIdx.x * (kGemvThreads / 32 / share) + warp / share, part = warp % share;
+  const bool real = n < a.N;
+  const int8_t* w = a.w + (int64_t)(real ? n : 0) * a.ldw;
+  const int whole = a.K / 16, rest = a.K % 16;   // 16-byte pieces of a row
+  int acc[MT] = {};
+  if (rest != 0 && part == 0 && lane == 0) {
+    const uint4 wv = row_end(w + 16 * whole, rest);
 #pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = a.w + (int64_t)min(n0 + r, a.N - 1) * a.ldw;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = a.x + (int64_t)min(m0 + m, a.M - 1) * a.ldx;
-  int acc[R][MT] = {};
-  constexpr int U = 8 / R;   // row loads in flight: 8 a lane
-  for (int k0 = 0; k0 < a.K; k0 += 512 * U) {
-    uint4 wv[U][R];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int k = k0 + 512 * u + 16 * lane;
-        wv[u][r] = k < a.K ? row_chunk<true>(w[r], k, a.K) : make_uint4(0, 0, 0, 0);
-      }
+    for (int m = 0; m < MT; ++m) acc[m] = dot16(wv, row_end(a.x + m * a.ldx + 16 * whole, rest), acc[m]);
+  }
+  constexpr int U = 8;
+  for (int base = part * 32; base < whole; base += 32 * share * U) {
+    uint4 wv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + 512 * u + 16 * lane;
-      if (k >= a.K) break;
+      const int c = base + 32 * share * u + lane;
+      wv[u] = chunk_if(w + 16 * c, c < whole);
+    }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const uint4 xv = row_chunk<false>(x[m], k, a.K);
+    for (int u = 0; u < U; ++u) {
+      const int c = base + 32 * share * u + lane;
+      if (c < whole) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][m] = dot16(wv[u][r], xv, acc[r][m]);
+        for (int m = 0; m < MT; ++m)
+          acc[m] = dot16(wv[u], __ldg(reinterpret_cast<const uint4*>(a.x + m * a.ldx) + c), acc[m]);
       }
     }
   }
-  // lane r + R m keeps the sum of row r and token m
-  int mine = 0;
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m) acc[m] = __reduce_add_sync(0xffffffffu, acc[m]);
+  if (share > 1) {
+    if (lane == 0) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int s = __reduce_add_sync(0xffffffffu, acc[r][m]);
-      if (lane == r + R * m) mine = s;
+      for (int m = 0; m < MT; ++m) parts[warp][m] = acc[m];
     }
-  const int n = n0 + lane % R, m = m0 + lane / R;
-  if (lane < R * MT && n < a.N && m < a.M)
-    store_y(a.y, a.y_type, (int64_t)m * a.ldy + n, scaled(mine, __ldg(a.x_scale + m), __ldg(a.w_scale + n), a.bias, n));
+    __syncthreads();
+    if (part != 0) return;
+    for (int i = 1; i < share; ++i) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m] += parts[warp + i][m];
+    }
+  }
+  if (lane < MT && real) {
+    int sum = acc[0];
+#pragma unroll
+    for (int m = 1; m < MT; ++m) sum = lane == m ? acc[m] : sum;
+    store_y(a.y, a.y_type, lane * a.ldy + n, scaled(sum, __ldg(a.x_scale + lane), __ldg(a.w_scale + n), a.bias, n));
+  }
 }
 
-template <int R, int MT>
+template <int MT>
 cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.N + 4 * R - 1) / (4 * R)), (unsigned)((a.M + MT - 1) / MT));
-  gemv_i8_kernel<R, MT><<<grid, 128, 0, stream>>>(a);
+  const int steps = (a.K + 511) / 512;
+  const int share = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, rows = kGemvThreads / 32 / share;
+  gemv_i8_kernel<MT><<<(unsigned)((a.N + rows - 1) / rows), kGemvThreads, 0, stream>>>(a, share);
   return cudaGetLastError();
 }
 
@@ -118,8 +132,9 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 // The channels are the rows of the MMA (A, 128 a CTA), the tokens its columns (B), so that a thread of the
 // epilogue owns one channel and a warp writes 32 neighbouring ones. A tile is 128 channels (256 for a
 // CTA pair) by tn tokens; its K is cut in blocks of 128 bytes, one stage of a ring each (TMA, 128-byte
-// swizzle, zeros behind the ends of K, M and N). Warps: 0 loads (TMA), 1 issues the MMAs, 2-5 are the
-// epilogue (TMEM lanes 32 (warp % 4) ..). Every wait is bounded.
+// swizzle, zeros behind the ends of K, M and N). Warps: 0 loads (TMA), 1 issues the MMAs, 2-9 are the
+// epilogue (two for each 32 TMEM lanes 32 (warp % 4) .., which take turns of 16 tokens). Every wait is
+// bounded.
 //
 // CTA pairs (cta_group::2) load each operand once for 256 x tn outputs. Two forms (plan_gemm_i8 chooses
 // by the time it expects of each):
@@ -128,7 +143,7 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 //               Two CTAs fit an SM.
 //   persistent  pairs take whole tiles in turn; the epilogue of a tile overlaps the products of the next
 //               (two accumulators).
-constexpr int kGemmThreads = 192;
+constexpr int kGemmThreads = 320, kEpilogueThreads = 256;
 constexpr int kMaxStages = 12;
 
 struct GemmBars {
@@ -234,11 +249,34 @@ __device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16],
   store16(a, m, left, ch, lane, v, bias);
 }
 
-// The scales of a tile's tokens, to shared memory, by the 128 threads of the epilogue.
+// The scales of a tile's tokens, to shared memory, by the threads of the epilogue.
 __device__ __forceinline__ void stage_scales(float* to, const float* x_scale, int cols, int tn, int t) {
-  for (int i = t; i < tn; i += 128) to[i] = i < cols ? __ldg(x_scale + i) : 0.f;
+  for (int i = t; i < tn; i += kEpilogueThreads) to[i] = i < cols ? __ldg(x_scale + i) : 0.f;
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueThreads) : "memory"); }
+
+// This warp's turns of 16 columns of an accumulator, f(first column, sums); the next turn's sums are on
+// their way from tensor memory while f works.
+template <typename F>
+__device__ __forceinline__ void each16(uint32_t acc, int turn, int cols, F f) {
+  float v[2][16];
+  int c0 = 16 * turn;
+  if (c0 < cols) tmem_ld16(acc + c0, v[0]);
+#pragma unroll 1
+  for (; c0 < cols; c0 += 64) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int c = c0 + 32 * b;
+      if (c >= cols) break;
+      tmem_wait_ld();
+      if (c + 32 < cols) tmem_ld16(acc + c + 32, v[b ^ 1]);
+      int sum[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[b][i]);
+      f(c, sum);
+    }
+  }
+}
 
 // The end of a split tile: all parts' sums lie in shared memory as [token][128 channels]. This part's tokens are
 // part, part + split, ...; a warp takes every sixth of them (four at a time, for loads in flight), a lane
@@ -321,7 +359,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   const int b_rows = p.tn / CG;                       // tokens that this CTA loads
   const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)b_rows * 128;
   volatile int* abort_flag = &bars.abort_flag;
-  const int q = warp & 3, row = 32 * q + lane, ch = n0 + row;
+  const int q = warp & 3, turn = warp >= 6, row = 32 * q + lane, ch = n0 + row;
   const int cols = min(p.tn, p.a.M - m0);   // tokens of this tile
   float ws = 0.f, bias = 0.f;
   __shared__ float xs[256];
@@ -334,7 +372,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
       prefetch_tensormap(&wmap);
       prefetch_tensormap(&xmap);
     }
-    init_bars(bars, p.stages, 4);
+    init_bars(bars, p.stages, 1);
     if (!PAIR && lane == 0) {
       for (int i = 0; i < p.stages && k_next < k1; ++i, ++k_next) {
         mbar_arrive_expect_tx(&bars.full[i], stage_bytes);
@@ -401,19 +439,15 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
       fence_after_sync();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
       int* mine = reinterpret_cast<int*>(ring) + row;   // [token][channel]; every copy has been consumed
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        float v[16];
-        int sum[16];
-        tmem_ld16(acc + c0, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
-        if (p.split == 1) {
+      if (p.split == 1) {
+        each16(acc, turn, cols, [&](int c0, const int (&sum)[16]) {
           finish16(p.a, sum, xs + c0, m0 + c0, cols - c0, ch, lane, ws, bias);
-        } else {
+        });
+      } else {
+        each16(acc, turn, cols, [&](int c0, const int (&sum)[16]) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[(c0 + i) * 128] = sum[i];
-        }
+        });
       }
     }
     fence_before_sync();
@@ -450,7 +484,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       prefetch_tensormap(&wmap);
       prefetch_tensormap(&xmap);
     }
-    init_bars(bars, p.stages, 8);
+    init_bars(bars, p.stages, 2 * kEpilogueThreads / 32);
   }
   if (warp == 1) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
   fence_before_sync();
@@ -498,7 +532,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, turn = warp >= 6;
     uint32_t n = 0;
     for (int t = worker; t < p.tiles; t += G, ++n) {
       const uint32_t d = n & 1;
@@ -512,15 +546,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
       fence_after_sync();
       const uint32_t acc = tmem + d * p.tn + ((uint32_t)(32 * q) << 16);
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        float v[16];
-        int sum[16];
-        tmem_ld16(acc + c0, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = __float_as_int(v[i]);
+      each16(acc, turn, cols, [&](int c0, const int (&sum)[16]) {
         finish16(p.a, sum, xs[d] + c0, m0 + c0, cols - c0, ch, lane, ws, bias);
-      }
+      });
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[d], 0));
@@ -534,6 +562,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
 constexpr int kSMs = 148;
 constexpr int kRing = 96 * 1024, kDeepRing = 208 * 1024;   // of a CTA that shares its SM with another, and of one that does not
+
+// Clusters of 1 .. 8 CTAs that run at once with one CTA an SM, and with two (a cluster stays inside a GPC, so
+// sizes that do not divide its SMs leave some idle; cudaOccupancyMaxActiveClusters on this part).
+constexpr int kClustersAlone[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+constexpr int kClustersShared[9] = {0, 296, 148, 93, 71, 56, 45, 37, 33};
 
 // Shared memory limits are set once per device and kernel.
 template <typename Kernel>
@@ -549,43 +582,61 @@ cudaError_t allow_smem(Kernel kern, int bytes, bool* done) {
   return cudaSuccess;
 }
 
+// Expected time of a plan in microseconds. The form follows the machine (bytes into an SM, clocks of the
+// tensor core, memory, a start and an end for each tile); the constants are fitted to the times of all
+// plans on 216 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). The plan it picks takes 4 % longer than
+// the best one, in the geometric mean; the largest plain choice (one CTA a tile, K whole) 24 %.
+double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
+  const int cg = 1 + p.pair, tn = p.tn;
+  // weights that several token tiles read are read once more now and then
+  const double memory = (1.36 * (p.mt > 1 ? 1.0 : 1 / 1.36) * N * K + M * K + 2.0 * M * N) / 5.5e6;
+  const double tensor = 2.0 * tn / 1900;                           // one block: 8192 products a clock
+  if (p.persistent) {
+    const int64_t rounds = (p.tiles + kSMs / 2 - 1) / (kSMs / 2);
+    const double block = std::max(tensor, (16384 + 64.0 * tn) / 100e3);
+    return 3.9 + std::max(rounds * std::max(p.kb * block, 0.021 * tn), memory) + 0.010 * tn;
+  }
+  const int c = cg * p.split;
+  const bool alone = p.tiles <= kClustersAlone[c];
+  const int64_t waves = alone ? 1 : (p.tiles + kClustersShared[c] - 1) / kClustersShared[c];
+  const int64_t even = ((int64_t)p.tiles * c + kSMs - 1) / kSMs;     // CTAs of an SM
+  const int64_t most = alone ? 1 : waves == 1 ? std::min<int64_t>(2, even) : std::max(2 * waves - 1, std::min(2 * waves, even));
+  const int blocks = (p.kb + p.split - 1) / p.split;
+  const double block = std::max(tensor, (16384 + 128.0 * tn / cg) / 118e3);
+  double t = 1.3 + 0.13 * p.pair + std::max(most * blocks * block, memory) + waves * 2.1;
+  t += p.split > 1 ? 0.5 + 0.02 * c * c + waves * 0.025 * tn : waves * 0.023 * tn;
+  return t;
+}
+
 }  // namespace
 
-// Expected times, in clocks of one SM. A block of 128 channels x tn tokens x 128 bytes of K takes
-// 2 tn clocks of the tensor core (8192 products a clock) and its operands come from L2 at about
-// kL2Bytes a clock; a tile has a start and an end (pipeline fill, epilogue, for a split tile the
-// exchange of sums), kTileClocks and 8 a token.
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
-  *p = GemmI8Plan{};
-  const int kb = (int)((K + 127) / 128);
-  p->kb = kb;
+  GemmI8Plan o{};
+  o.kb = (int)((K + 127) / 128);
   double best = 0;
-  constexpr double kL2Bytes = 48;
+  bool any = false;
+  auto offer = [&] {
+    const double t = expected_us(o, M, N, K);
+    if (any && t >= best) return;
+    any = true;
+    best = t;
+    *p = o;
+  };
   const int64_t mt0 = (M + 255) / 256, mt1 = std::min<int64_t>((M + 15) / 16, mt0 + 7);
   for (int64_t mt = mt0; mt <= mt1; ++mt) {
-    for (int pair = 0; pair < (N > 128 && M > 16 ? 2 : 1); ++pair) {
-      const int cg = 1 + pair, step = 16 * cg;
-      const int tn = (int)(((M + mt - 1) / mt + step - 1) / step * step);
-      const int64_t mtiles = (M + tn - 1) / tn, tiles = mtiles * ((N + 128 * cg - 1) / (128 * cg));
+    for (o.pair = 0; o.pair < (N > 128 ? 2 : 1); ++o.pair) {
+      const int cg = 1 + o.pair, step = 16 * cg;
+      o.tn = (int)(((M + mt - 1) / mt + step - 1) / step * step);
+      o.mt = (int)((M + o.tn - 1) / o.tn);
+      const int64_t tiles = o.mt * ((N + 128 * cg - 1) / (128 * cg));
       if (tiles > (1 << 26)) return false;
-      const double block = std::max(2.0 * tn, (16384 + 128.0 * tn / cg) / kL2Bytes);
-      auto offer = [&](int persistent, int split, double t) {
-        if (p->tn != 0 && t >= best) return;
-        best = t;
-        p->pair = pair;
-        p->persistent = persistent;
-        p->tn = tn;
-        p->mt = (int)mtiles;
-        p->tiles = (int)tiles;
-        p->split = split;
-      };
-      for (int s = 1; s <= std::min(8 / cg, kb); ++s) {
-        const int64_t rounds = (tiles * s * cg + kSMs - 1) / kSMs;
-        offer(0, s, rounds * ((kb + s - 1) / s) * block + (rounds + 1) / 2 * (1500 + 8.0 * tn) + (s > 1 ? 800 + 4.0 * tn : 0));
-      }
-      if (pair) {
-        const int64_t rounds = (tiles + kSMs / 2 - 1) / (kSMs / 2);
-        offer(1, 1, rounds * std::max((double)kb * block, 500 + 12.0 * tn) + 2000 + 12.0 * tn);
+      o.tiles = (int)tiles;
+      o.persistent = 0;
+      for (o.split = 1; o.split <= std::min(8 / cg, o.kb); ++o.split) offer();
+      o.split = 1;
+      if (o.pair) {
+        o.persistent = 1;
+        offer();
       }
     }
   }
@@ -604,8 +655,8 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   const int stage = 128 * 128 + pl.tn / cg * 128;
   const int cluster = pl.persistent ? 2 : cg * pl.split;
   const int64_t ctas = (int64_t)(pl.persistent ? std::min(pl.tiles, kSMs / 2) : pl.tiles) * cluster;
-  // a CTA that has its SM for itself takes the deeper ring
-  const int room = pl.persistent || ctas <= kSMs ? kDeepRing : kRing;
+  // CTAs that have an SM for themselves take the deeper ring
+  const int room = pl.persistent || pl.tiles <= kClustersAlone[cluster] ? kDeepRing : kRing;
   p.stages = std::min({kMaxStages, room / stage, std::max(1, (pl.kb + pl.split - 1) / pl.split * (pl.persistent ? kMaxStages : 1))});
   p.tmem_cols = 32;
   while (p.tmem_cols < (pl.persistent ? 2 : 1) * pl.tn) p.tmem_cols *= 2;   // two accumulators in the persistent form
@@ -634,10 +685,7 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {
-  if (a.M == 1) return run_gemv<1, 1>(a, stream);
-  if (a.M == 2) return run_gemv<2, 2>(a, stream);
-  if (a.M <= 4) return run_gemv<4, 4>(a, stream);
-  return run_gemv<4, 8>(a, stream);
+  return a.M == 1 ? run_gemv<1>(a, stream) : run_gemv<2>(a, stream);
 }
 
 }  // namespace wr

@@ -48,7 +48,7 @@ struct GemmI8Plan {
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
 // Tokens up to which the product runs on dp4a, without a workspace.
-constexpr int kGemvI8Tokens = 8;
+constexpr int kGemvI8Tokens = 2;
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);
 cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream);
 // Sums of K products of int8 values stay inside int32 up to this K ((-128)^2 * K < 2^31).

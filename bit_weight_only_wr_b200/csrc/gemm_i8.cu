@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(kGemvThreads) gemv_i8_kernel(const GemmI8Args 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = blockIdx.x * (kGemvThreads / 32 / share) + warp / share, part = warp % share;
   const bool real = n < a.N;
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int8_t* w = a.w + (int64_t)(real ? n : 0) * a.ldw;
   const int whole = a.K / 16, rest = a.K % 16;   // 16-byte pieces of a row
   int acc[MT] = {};
@@ -123,8 +125,7 @@ template <int MT>
 cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
   const int steps = (a.K + 511) / 512;
   const int share = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, rows = kGemvThreads / 32 / share;
-  gemv_i8_kernel<MT><<<(unsigned)((a.N + rows - 1) / rows), kGemvThreads, 0, stream>>>(a, share);
-  return cudaGetLastError();
+  return launch_overlapped(gemv_i8_kernel<MT>, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kGemvThreads), 0, 1, stream, a, share);
 }
 
 // ---------------------------------------------------------------- more tokens: tcgen05 kind::i8
@@ -367,12 +368,14 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   // A CTA of its own fills the ring before it meets the other warps; a pair's copies complete on the
   // leader's barriers, which have to be there first.
   int k_next = k0;
+  grid_launch_dependents();
   if (warp == 0) {
     if (lane == 0) {
       prefetch_tensormap(&wmap);
       prefetch_tensormap(&xmap);
     }
     init_bars(bars, p.stages, 1);
+    grid_dependency_wait();
     if (!PAIR && lane == 0) {
       for (int i = 0; i < p.stages && k_next < k1; ++i, ++k_next) {
         mbar_arrive_expect_tx(&bars.full[i], stage_bytes);
@@ -383,7 +386,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   } else if (warp == 1) {
     if (PAIR) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
     else tmem_alloc(&bars.tmem_base, p.tmem_cols);
+    grid_dependency_wait();
   } else {
+    grid_dependency_wait();
     stage_scales(xs, p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
     if (ch < p.a.N) {
       ws = __ldg(p.a.w_scale + ch);
@@ -486,8 +491,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     init_bars(bars, p.stages, 2 * kEpilogueThreads / 32);
   }
+  grid_launch_dependents();
   if (warp == 1) tmem_alloc_pair(&bars.tmem_base, p.tmem_cols);
   fence_before_sync();
+  grid_dependency_wait();
   cluster_sync();
   fence_after_sync();
   const uint32_t tmem = bars.tmem_base;
@@ -670,18 +677,7 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   if (e != cudaSuccess) return e;
   // the ring, or the sums that replace it at the end of a split tile
   const int ring = std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = (size_t)ring + 1024;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p, wmap, xmap);
+  return launch_overlapped(kern, dim3((unsigned)ctas), dim3(kGemmThreads), (size_t)ring + 1024, cluster, stream, p, wmap, xmap);
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {

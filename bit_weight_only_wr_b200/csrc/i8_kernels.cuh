@@ -7,6 +7,31 @@
 
 namespace wr {
 
+// Launches a product so that it may start while the kernel before it in the stream still runs: its CTAs set up
+// barriers and tensor memory and then wait in grid_dependency_wait() before they touch memory that
+// another kernel may write or read. In a graph of such calls o of one token takes 3.6 us instead of
+// 3.9, q/k/v of 32 tokens 7.1 instead of 7.6, down of 333 tokens 13.4 instead of 14.6; norm and q/k/v of
+// 32 tokens together 10.6 instead of 11.4. (The row operators are launched plainly: their many small
+// CTAs, started early, took slots from the kernel before; 8192 rows 45 instead of 40 us.)
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
+                                     const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Row quantizer: v = x (or silu(gate) x), one fp32 scale and int8 codes per row.
 struct QuantRowsArgs {
   const uint8_t* x;

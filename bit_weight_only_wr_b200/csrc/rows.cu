@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "i8_kernels.cuh"
+#include "tc_common.cuh"
 
 namespace wr {
 namespace {
@@ -345,6 +346,7 @@ __global__ void __launch_bounds__(MAXT) quantize_rows_kernel(const QuantRowsArgs
   __shared__ uint32_t buf[32];
   const int T = blockDim.x, t = threadIdx.x;
   const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  tc::grid_launch_dependents();   // a product that follows may set itself up meanwhile
   if (m >= a.M) return;   // (whole warps)
   constexpr int es = F32 ? 4 : 2;
   const uint8_t* x = a.x + m * a.ldx * es;
@@ -399,6 +401,7 @@ __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) 
   __shared__ uint32_t buf_max[32];
   const int T = blockDim.x, t = threadIdx.x, D = (int)a.D;
   const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  tc::grid_launch_dependents();   // a product that follows may set itself up meanwhile
   if (m >= a.M) return;   // (whole warps)
   const uint8_t* b = static_cast<const uint8_t*>(a.block) + m * a.ld_block * (B32 ? 4 : 2);
   const uint8_t* h = static_cast<const uint8_t*>(a.residual) + m * a.ld_residual * (R32 ? 4 : 2);
@@ -494,7 +497,8 @@ inline bool rows_aligned(int64_t M, int64_t ld, int bytes) { return M == 1 || ld
 // Threads that hold a row of D elements, VPT vectors of 8 each.
 inline int row_threads(int64_t D, int vpt) { return (int)std::min<int64_t>(1024, ((D + 8 * vpt - 1) / (8 * vpt) + 31) / 32 * 32); }
 
-// Vectors a thread. Few rows: one, the shortest way through a row. Many: two, since a thread's work in the
+// Vectors a thread. Few rows: one or two, the shortest way through a row (one gated row of 9728 fp32 values:
+// 3.2 us with two, 3.9 with four). Many: two, since a thread's work in the
 // reductions is the same for 16 elements as for 8 and instructions run out before bandwidth does, while
 // four leave too few warps to hide the loads (8192 rows of 2560, fp32 block, bf16 residual: 48.0, 37.5 and
 // 58.8 us with one, two and four; 500 rows: 5.0, 4.6 and 6.6). Four where two would make a CTA of more
@@ -503,7 +507,8 @@ inline int row_threads(int64_t D, int vpt) { return (int)std::min<int64_t>(1024,
 constexpr int64_t kManyRows = 2 * 148;
 inline int row_vpt(int64_t M, int64_t D, int most) {
   const int64_t vecs = (D + 7) / 8;
-  return vecs > 2 * most ? 4 : vecs <= (M < kManyRows ? 512 : 32) ? 1 : 2;
+  if (M < kManyRows) return vecs <= 512 ? 1 : vecs <= 2048 ? 2 : 4;
+  return vecs <= 32 ? 1 : vecs <= 2 * most ? 2 : 4;
 }
 // The launch: a CTA for each row, or, where a warp holds a row, four rows a CTA.
 struct RowGrid {
@@ -516,7 +521,7 @@ struct RowGrid {
 };
 
 template <int VPT, int MAXT, bool VEC>
-void run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
+cudaError_t run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
   const RowGrid d(a.M, row_threads(a.K, VPT > 0 ? VPT : 4));
   if (a.type == WR_F32) {
     if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, true, true><<<d.grid, d.block, 0, stream>>>(a);
@@ -525,38 +530,40 @@ void run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
     if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, false, true><<<d.grid, d.block, 0, stream>>>(a);
     else quantize_rows_kernel<VPT, MAXT, VEC, false, false><<<d.grid, d.block, 0, stream>>>(a);
   }
+  return cudaGetLastError();
 }
 template <bool VEC>
-void run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
+cudaError_t run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
   const int vpt = row_vpt(a.M, a.K, 256);
-  if (a.K > 32768) run_quantize<0, 1024, VEC>(a, stream);
-  else if (a.K > 16384) run_quantize<4, 1024, VEC>(a, stream);
-  else if (vpt == 1) run_quantize<1, 512, VEC>(a, stream);
-  else if (vpt == 2) run_quantize<2, 512, VEC>(a, stream);
-  else run_quantize<4, 512, VEC>(a, stream);
+  if (a.K > 32768) return run_quantize<0, 1024, VEC>(a, stream);
+  if (a.K > 16384) return run_quantize<4, 1024, VEC>(a, stream);
+  if (vpt == 1) return run_quantize<1, 512, VEC>(a, stream);
+  if (vpt == 2) return a.K <= 8192 ? run_quantize<2, 512, VEC>(a, stream) : run_quantize<2, 1024, VEC>(a, stream);
+  return run_quantize<4, 512, VEC>(a, stream);
 }
 
 template <int VPT, int MAXT, bool VEC, bool B32, bool R32>
-void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+cudaError_t run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
   const RowGrid d(a.p.M, row_threads(a.p.D, VPT));
   if (w32) residual_norm_kernel<VPT, MAXT, VEC, B32, R32, true><<<d.grid, d.block, 0, stream>>>(a);
   else residual_norm_kernel<VPT, MAXT, VEC, B32, R32, false><<<d.grid, d.block, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 template <int VPT, int MAXT, bool VEC>
-void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+cudaError_t run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
   const bool b32 = a.p.block_type == WR_F32, r32 = a.p.residual_type == WR_F32;
-  if (b32 && r32) run_norm<VPT, MAXT, VEC, true, true>(a, w32, stream);
-  else if (b32) run_norm<VPT, MAXT, VEC, true, false>(a, w32, stream);
-  else if (r32) run_norm<VPT, MAXT, VEC, false, true>(a, w32, stream);
-  else run_norm<VPT, MAXT, VEC, false, false>(a, w32, stream);
+  if (b32 && r32) return run_norm<VPT, MAXT, VEC, true, true>(a, w32, stream);
+  else if (b32) return run_norm<VPT, MAXT, VEC, true, false>(a, w32, stream);
+  else if (r32) return run_norm<VPT, MAXT, VEC, false, true>(a, w32, stream);
+  else return run_norm<VPT, MAXT, VEC, false, false>(a, w32, stream);
 }
 template <bool VEC>
-void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
+cudaError_t run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
   const int vpt = row_vpt(a.p.M, a.p.D, 512);
-  if (a.p.D > 16384) run_norm<4, 1024, VEC>(a, w32, stream);
-  else if (vpt == 1) run_norm<1, 512, VEC>(a, w32, stream);
-  else if (vpt == 2) run_norm<2, 512, VEC>(a, w32, stream);
-  else run_norm<4, 512, VEC>(a, w32, stream);
+  if (a.p.D > 16384) return run_norm<4, 1024, VEC>(a, w32, stream);
+  if (vpt == 1) return run_norm<1, 512, VEC>(a, w32, stream);
+  if (vpt == 2) return a.p.D <= 8192 ? run_norm<2, 512, VEC>(a, w32, stream) : run_norm<2, 1024, VEC>(a, w32, stream);
+  return run_norm<4, 512, VEC>(a, w32, stream);
 }
 
 }  // namespace
@@ -564,9 +571,7 @@ void run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
 cudaError_t launch_quantize_rows(const QuantRowsArgs& a, cudaStream_t stream) {
   const int es = type_bytes(a.type);
   const bool vec = rows_aligned(a.M, a.ldx, es) && (!a.gate || rows_aligned(a.M, a.ldg, es)) && (a.M == 1 || a.ldq % 8 == 0);
-  if (vec) run_quantize<true>(a, stream);
-  else run_quantize<false>(a, stream);
-  return cudaGetLastError();
+  return vec ? run_quantize<true>(a, stream) : run_quantize<false>(a, stream);
 }
 
 cudaError_t launch_residual_norm(const wr_residual_norm_args& a, cudaStream_t stream) {
@@ -577,9 +582,7 @@ cudaError_t launch_residual_norm(const wr_residual_norm_args& a, cudaStream_t st
                    (!a.y || (a.y_type == WR_I8 ? a.M == 1 || a.ld_y % 8 == 0 : rows_aligned(a.M, a.ld_y, type_bytes(a.y_type))));
   NormArgs na{a, (float)(1.0 / (double)a.D)};
   const bool w32 = a.post_weight || a.norm_weight ? a.weight_type == WR_F32 : a.gate_type == WR_F32;
-  if (vec) run_norm<true>(na, w32, stream);
-  else run_norm<false>(na, w32, stream);
-  return cudaGetLastError();
+  return vec ? run_norm<true>(na, w32, stream) : run_norm<false>(na, w32, stream);
 }
 
 }  // namespace wr

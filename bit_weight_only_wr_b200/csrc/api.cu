@@ -702,7 +702,7 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
   if (!aligned16(x) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || (bias && !aligned16(bias)) ||
       !aligned16(y))
     return WR_ERR_INVALID_ARG;
-  const bool few = M <= wr::kGemvI8Tokens;
+  const bool few = wr::gemv_i8_pays(M, N, K);
   wr::GemmI8Plan plan{};
   if (!few && !wr::plan_gemm_i8(M, N, K, &plan)) return WR_ERR_INVALID_ARG;
   (void)workspace;

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "i8_kernels.cuh"
@@ -20,7 +21,7 @@ using namespace tc;
 
 __device__ __forceinline__ float scaled(int acc, float xs, float ws, const float* bias, int n) {
   const float v = (float)acc * xs * ws;
-  return bias ? v + __ldg(bias + n) : v;
+  return bias ? v + bias[n] : v;
 }
 __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v) {
   if (type == WR_F32) static_cast<float*>(y)[at] = v;
@@ -30,24 +31,30 @@ __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v) 
 
 // ---------------------------------------------------------------- one or two tokens: dp4a, one pass over w
 
-// 16 bytes, or zeros (no load) where !in.
+// 16 bytes, or zeros (no load) where !in; KEEP: in L1 too. (None of these kernels reads through the read-only
+// path: they may start before the kernel that writes their inputs has ended, see launch_overlapped.)
+template <bool KEEP>
 __device__ __forceinline__ uint4 chunk_if(const int8_t* p, bool in) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-      : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-      : "l"(p), "r"((int)in));
+  if (KEEP)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "l"(p), "r"((int)in));
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "l"(p), "r"((int)in));
   return v;
 }
 // The last `n` < 16 bytes of a row (p 16-byte aligned), then zeros: whole words, then single bytes.
 __device__ __forceinline__ uint4 row_end(const int8_t* p, int n) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = 4 * i + 4 <= n ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : 0u;
+  for (int i = 0; i < 4; ++i) w[i] = 4 * i + 4 <= n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
   uint32_t rest = 0;
 #pragma unroll
   for (int i = 0; i < 3; ++i)
-    if ((n & ~3) + i < n) rest |= (uint32_t)(uint8_t)__ldg(p + (n & ~3) + i) << (8 * i);
+    if ((n & ~3) + i < n) rest |= (uint32_t)(uint8_t)p[(n & ~3) + i] << (8 * i);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i == n / 4) w[i] = rest;
@@ -63,61 +70,73 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
 
 // `share` warps (1, 2 or 4) of a CTA share a row of w and read it once, 512 bytes a warp and step with eight
 // steps in flight; x comes from L1. Memory latency is what a matrix of this size is bound by, so share is
-// what lets a warp have all of its bytes on their way at once (up to K = 16384).
-constexpr int kGemvThreads = 128;
+// what lets a warp have all of its bytes on their way at once (up to K = 16384). Where there are rows for more
+// than two rounds of CTAs, a CTA takes rows in turn (19456 rows of 2560: 9.2 us, a CTA for every four rows
+// 10.0; 6144 rows: 4.6 and 3.7).
+constexpr int kGemvThreads = 128, kGemvCtas = 148 * 9;   // nine CTAs fill an SM's registers
 template <int MT>
-__global__ void __launch_bounds__(kGemvThreads) gemv_i8_kernel(const GemmI8Args a, const int share) {
-  __shared__ int parts[kGemvThreads / 32][MT];
+__global__ void __launch_bounds__(kGemvThreads, 9) gemv_i8_kernel(const GemmI8Args a, const int share) {
+  __shared__ int parts[2][kGemvThreads / 32][MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n = blockIdx.x * (kGemvThreads / 32 / share) + warp / share, part = warp % share;
-  const bool real = n < a.N;
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int8_t* w = a.w + (int64_t)(real ? n : 0) * a.ldw;
+  const int rows = kGemvThreads / 32 / share, part = warp % share;
   const int whole = a.K / 16, rest = a.K % 16;   // 16-byte pieces of a row
-  int acc[MT] = {};
-  if (rest != 0 && part == 0 && lane == 0) {
-    const uint4 wv = row_end(w + 16 * whole, rest);
+  int n = blockIdx.x * rows + warp / share;
+  grid_launch_dependents();
+  // the first row may come to L2 while the kernel before this one still runs
+  if (n < a.N)
+    for (int k = (part * 32 + lane) * 128; k < a.K; k += share * 4096) prefetch_l2(a.w + (int64_t)n * a.ldw + k);
+  grid_dependency_wait();
+  const float xs = a.x_scale[min(lane, MT - 1)];
+  for (int first = blockIdx.x * rows, par = 0; first < a.N; first += gridDim.x * rows, n += gridDim.x * rows, par ^= 1) {
+    const bool real = n < a.N;
+    const int8_t* w = a.w + (int64_t)(real ? n : 0) * a.ldw;
+    const float ws = real ? a.w_scale[n] : 0.f;
+    int acc[MT] = {};
+    if (rest != 0 && part == 0 && lane == 0) {
+      const uint4 wv = row_end(w + 16 * whole, rest);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = dot16(wv, row_end(a.x + m * a.ldx + 16 * whole, rest), acc[m]);
-  }
-  constexpr int U = 8;
-  for (int base = part * 32; base < whole; base += 32 * share * U) {
-    uint4 wv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = base + 32 * share * u + lane;
-      wv[u] = chunk_if(w + 16 * c, c < whole);
+      for (int m = 0; m < MT; ++m) acc[m] = dot16(wv, row_end(a.x + m * a.ldx + 16 * whole, rest), acc[m]);
     }
+    constexpr int U = 8;
+    for (int base = part * 32; base < whole; base += 32 * share * U) {
+      uint4 wv[U], xv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = base + 32 * share * u + lane;
-      if (c < whole) {
+      for (int u = 0; u < U; ++u) {
+        const int c = base + 32 * share * u + lane;
+        wv[u] = chunk_if<false>(w + 16 * c, c < whole);
+      }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          acc[m] = dot16(wv[u], __ldg(reinterpret_cast<const uint4*>(a.x + m * a.ldx) + c), acc[m]);
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = base + 32 * share * u + lane;
+          xv[u] = chunk_if<true>(a.x + m * a.ldx + 16 * c, c < whole);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[m] = dot16(wv[u], xv[u], acc[m]);
       }
     }
-  }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = __reduce_add_sync(0xffffffffu, acc[m]);
-  if (share > 1) {
-    if (lane == 0) {
+    for (int m = 0; m < MT; ++m) acc[m] = __reduce_add_sync(0xffffffffu, acc[m]);
+    if (share > 1) {
+      if (lane == 0) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) parts[warp][m] = acc[m];
+        for (int m = 0; m < MT; ++m) parts[par][warp][m] = acc[m];
+      }
+      __syncthreads();   // (the other buffer was read before this barrier and is written after it)
+      if (part == 0) {
+        for (int i = 1; i < share; ++i) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m] += parts[par][warp + i][m];
+        }
+      }
     }
-    __syncthreads();
-    if (part != 0) return;
-    for (int i = 1; i < share; ++i) {
+    if (lane < MT && part == 0 && real) {
+      int sum = acc[0];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m] += parts[warp + i][m];
+      for (int m = 1; m < MT; ++m) sum = lane == m ? acc[m] : sum;
+      store_y(a.y, a.y_type, lane * a.ldy + n, scaled(sum, xs, ws, a.bias, n));
     }
-  }
-  if (lane < MT && real) {
-    int sum = acc[0];
-#pragma unroll
-    for (int m = 1; m < MT; ++m) sum = lane == m ? acc[m] : sum;
-    store_y(a.y, a.y_type, lane * a.ldy + n, scaled(sum, __ldg(a.x_scale + lane), __ldg(a.w_scale + n), a.bias, n));
   }
 }
 
@@ -125,7 +144,8 @@ template <int MT>
 cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
   const int steps = (a.K + 511) / 512;
   const int share = steps <= 8 ? 1 : steps <= 16 ? 2 : 4, rows = kGemvThreads / 32 / share;
-  return launch_overlapped(gemv_i8_kernel<MT>, dim3((unsigned)((a.N + rows - 1) / rows)), dim3(kGemvThreads), 0, 1, stream, a, share);
+  const int ctas = (a.N + rows - 1) / rows, grid = ctas <= 2 * kGemvCtas ? ctas : kGemvCtas;
+  return launch_overlapped(gemv_i8_kernel<MT>, dim3((unsigned)grid), dim3(kGemvThreads), 0, 1, stream, a, share);
 }
 
 // ---------------------------------------------------------------- more tokens: tcgen05 kind::i8
@@ -141,7 +161,7 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 // by the time it expects of each):
 //   split       a cluster of `split` CTAs, or pairs, shares a tile, each with its part of K; they leave their
 //               int32 sums in shared memory and each finishes its part of the tokens from all of them.
-//               Two CTAs fit an SM.
+//               (Without a cluster two CTAs fit an SM.)
 //   persistent  pairs take whole tiles in turn; the epilogue of a tile overlaps the products of the next
 //               (two accumulators).
 constexpr int kGemmThreads = 320, kEpilogueThreads = 256;
@@ -252,7 +272,7 @@ __device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16],
 
 // The scales of a tile's tokens, to shared memory, by the threads of the epilogue.
 __device__ __forceinline__ void stage_scales(float* to, const float* x_scale, int cols, int tn, int t) {
-  for (int i = t; i < tn; i += kEpilogueThreads) to[i] = i < cols ? __ldg(x_scale + i) : 0.f;
+  for (int i = t; i < tn; i += kEpilogueThreads) to[i] = i < cols ? x_scale[i] : 0.f;
 }
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueThreads) : "memory"); }
 
@@ -280,7 +300,7 @@ __device__ __forceinline__ void each16(uint32_t acc, int turn, int cols, F f) {
 }
 
 // The end of a split tile: all parts' sums lie in shared memory as [token][128 channels]. This part's tokens are
-// part, part + split, ...; a warp takes every sixth of them (four at a time, for loads in flight), a lane
+// part, part + split, ...; a warp takes every tenth of them (four at a time, for loads in flight), a lane
 // four neighbouring channels.
 template <int CG>
 __device__ __forceinline__ void exchange(const GemmParams& p, const uint8_t* ring, const float* xs, int part, int half, int n0, int m0,
@@ -290,8 +310,8 @@ __device__ __forceinline__ void exchange(const GemmParams& p, const uint8_t* rin
   float ws[4], bias[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    ws[e] = e < real ? __ldg(p.a.w_scale + ch + e) : 0.f;
-    bias[e] = p.a.bias && e < real ? __ldg(p.a.bias + ch + e) : 0.f;
+    ws[e] = e < real ? p.a.w_scale[ch + e] : 0.f;
+    bias[e] = p.a.bias && e < real ? p.a.bias[ch + e] : 0.f;
   }
   const bool whole = real == 4 && (p.a.ldy & 3) == 0;        // four channels in one store
   for (int c0 = part + p.split * warp; c0 < cols; c0 += p.split * kWarps * kBatch) {
@@ -391,8 +411,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     grid_dependency_wait();
     stage_scales(xs, p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
     if (ch < p.a.N) {
-      ws = __ldg(p.a.w_scale + ch);
-      if (p.a.bias) bias = __ldg(p.a.bias + ch);
+      ws = p.a.w_scale[ch];
+      if (p.a.bias) bias = p.a.bias[ch];
     }
   }
   fence_before_sync();
@@ -546,8 +566,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int rg = t / p.mt, mt = t - rg * p.mt;
       const int ch = (rg * 2 + (int)rank) * 128 + 32 * q + lane, m0 = mt * p.tn;
       const int cols = min(p.tn, p.a.M - m0);         // tokens of this tile
-      const float ws = ch < p.a.N ? __ldg(p.a.w_scale + ch) : 0.f;
-      const float bias = p.a.bias && ch < p.a.N ? __ldg(p.a.bias + ch) : 0.f;
+      const float ws = ch < p.a.N ? p.a.w_scale[ch] : 0.f;
+      const float bias = p.a.bias && ch < p.a.N ? p.a.bias[ch] : 0.f;
       stage_scales(xs[d], p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
       epilogue_sync();   // (xs[d] was last read two tiles ago, before the other one's barrier)
       if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
@@ -568,16 +588,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 }
 
 constexpr int kSMs = 148;
-constexpr int kRing = 96 * 1024, kDeepRing = 208 * 1024;   // of a CTA that shares its SM with another, and of one that does not
 
-// Clusters of 1 .. 8 CTAs that run at once with one CTA an SM, and with two (a cluster stays inside a GPC, so
-// sizes that do not divide its SMs leave some idle; cudaOccupancyMaxActiveClusters on this part).
-constexpr int kClustersAlone[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
-constexpr int kClustersShared[9] = {0, 296, 148, 93, 71, 56, 45, 37, 33};
+// Shared memory of a CTA. A CTA that finds too little tensor memory waits until another one leaves; the CTAs of
+// a cluster wait for one another. Two clusters (calls on two streams) that held tensor memory on one SM each
+// and waited for it on the other's would wait for good. So a CTA of a cluster claims its SM's shared memory
+// whole and never meets another of these CTAs there; one on its own claims as large a share as of the
+// tensor memory (222 KB for 512 columns), so that whatever fits the SM finds its columns. The ring takes what
+// the claim allows.
+constexpr int kClaimPerColumn = 222 * 1024 / 512;
+constexpr int kRing = 256 * kClaimPerColumn - 1024, kDeepRing = 512 * kClaimPerColumn - 1024;   // (1024: alignment)
+
+// Clusters of 1 .. 8 CTAs that run at once with one CTA an SM (a cluster stays inside a GPC, so sizes that do
+// not divide its SMs leave some idle; cudaOccupancyMaxActiveClusters on this part).
+constexpr int kClusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 
 // Shared memory limits are set once per device and kernel.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, int bytes, bool* done) {
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool>* done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -591,8 +618,9 @@ cudaError_t allow_smem(Kernel kern, int bytes, bool* done) {
 
 // Expected time of a plan in microseconds. The form follows the machine (bytes into an SM, clocks of the
 // tensor core, memory, a start and an end for each tile); the constants are fitted to the times of all
-// plans on 216 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). The plan it picks takes 4 % longer than
-// the best one, in the geometric mean; the largest plain choice (one CTA a tile, K whole) 24 %.
+// plans on 216 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). On 96 other shapes the plan it picked took
+// 3 % longer than the best one in the geometric mean, and one CTA a tile with the fewest token tiles and
+// K whole 47 %.
 double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
   const int cg = 1 + p.pair, tn = p.tn;
   // weights that several token tiles read are read once more now and then
@@ -603,15 +631,14 @@ double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
     const double block = std::max(tensor, (16384 + 64.0 * tn) / 100e3);
     return 3.9 + std::max(rounds * std::max(p.kb * block, 0.021 * tn), memory) + 0.010 * tn;
   }
-  const int c = cg * p.split;
-  const bool alone = p.tiles <= kClustersAlone[c];
-  const int64_t waves = alone ? 1 : (p.tiles + kClustersShared[c] - 1) / kClustersShared[c];
-  const int64_t even = ((int64_t)p.tiles * c + kSMs - 1) / kSMs;     // CTAs of an SM
-  const int64_t most = alone ? 1 : waves == 1 ? std::min<int64_t>(2, even) : std::max(2 * waves - 1, std::min(2 * waves, even));
+  // two CTAs on their own share an SM; clusters run at once
+  const bool alone = p.tiles <= kClusters[cg * p.split];
+  const int64_t waves = alone ? 1 : (p.tiles + 2 * kSMs - 1) / (2 * kSMs), even = (p.tiles + kSMs - 1) / kSMs;
+  const int64_t most = alone ? 1 : std::max(2 * waves - 1, std::min(2 * waves, even));   // CTAs of the busiest SM
   const int blocks = (p.kb + p.split - 1) / p.split;
   const double block = std::max(tensor, (16384 + 128.0 * tn / cg) / 118e3);
   double t = 1.3 + 0.13 * p.pair + std::max(most * blocks * block, memory) + waves * 2.1;
-  t += p.split > 1 ? 0.5 + 0.02 * c * c + waves * 0.025 * tn : waves * 0.023 * tn;
+  t += p.split > 1 ? 0.5 + 0.02 * cg * cg * p.split * p.split + waves * 0.025 * tn : waves * 0.023 * tn;
   return t;
 }
 
@@ -639,7 +666,8 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
       if (tiles > (1 << 26)) return false;
       o.tiles = (int)tiles;
       o.persistent = 0;
-      for (o.split = 1; o.split <= std::min(8 / cg, o.kb); ++o.split) offer();
+      for (o.split = 1; o.split <= std::min(8 / cg, o.kb); ++o.split)
+        if (cg * o.split == 1 || o.tiles <= kClusters[cg * o.split]) offer();
       o.split = 1;
       if (o.pair) {
         o.persistent = 1;
@@ -663,7 +691,7 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   const int cluster = pl.persistent ? 2 : cg * pl.split;
   const int64_t ctas = (int64_t)(pl.persistent ? std::min(pl.tiles, kSMs / 2) : pl.tiles) * cluster;
   // CTAs that have an SM for themselves take the deeper ring
-  const int room = pl.persistent || pl.tiles <= kClustersAlone[cluster] ? kDeepRing : kRing;
+  const int room = cluster > 1 || pl.tiles <= kClusters[1] ? kDeepRing : kRing;
   p.stages = std::min({kMaxStages, room / stage, std::max(1, (pl.kb + pl.split - 1) / pl.split * (pl.persistent ? kMaxStages : 1))});
   p.tmem_cols = 32;
   while (p.tmem_cols < (pl.persistent ? 2 : 1) * pl.tn) p.tmem_cols *= 2;   // two accumulators in the persistent form
@@ -672,12 +700,13 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg))
     return cudaErrorInvalidValue;
   const auto kern = pl.persistent ? gemm_i8_persistent_kernel : pl.pair ? gemm_i8_split_kernel<true> : gemm_i8_split_kernel<false>;
-  static bool done[3][64];
+  static std::atomic<bool> done[3][64];
   const cudaError_t e = allow_smem(kern, kDeepRing + 1024, done[pl.persistent ? 2 : pl.pair]);
   if (e != cudaSuccess) return e;
   // the ring, or the sums that replace it at the end of a split tile
   const int ring = std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
-  return launch_overlapped(kern, dim3((unsigned)ctas), dim3(kGemmThreads), (size_t)ring + 1024, cluster, stream, p, wmap, xmap);
+  const int smem = std::max(ring + 1024, (cluster > 1 ? 512 : p.tmem_cols) * kClaimPerColumn);
+  return launch_overlapped(kern, dim3((unsigned)ctas), dim3(kGemmThreads), (size_t)smem, cluster, stream, p, wmap, xmap);
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {

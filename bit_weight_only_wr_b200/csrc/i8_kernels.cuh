@@ -72,8 +72,10 @@ struct GemmI8Plan {
   int tiles;
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
-// Tokens up to which the product runs on dp4a, without a workspace.
-constexpr int kGemvI8Tokens = 2;
+// One or two tokens run on dp4a where rows are few or long (2560 rows of 4096: 2.7 us a call, on the tensor cores
+// 5.1); many short rows cost it more than a tile does (16384 rows of 1024: 6.7 and 5.2 us, 8192 of 2048: 4.6
+// and 5.8).
+inline bool gemv_i8_pays(int64_t M, int64_t N, int64_t K) { return M <= 2 && (K > 1024 || N <= 4096); }
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);
 cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream);
 // Sums of K products of int8 values stay inside int32 up to this K ((-128)^2 * K < 2^31).

@@ -651,3 +651,34 @@ def test_host_tensors_are_refused(wr):
     x, q, s = torch.randn(2, 32), torch.empty(2, 32, dtype=torch.int8, device="cuda"), torch.empty(2, device="cuda")
     with pytest.raises(ValueError):
         wr.wr_quantize_rows(wr.WR_F32, 2, 32, x, 32, q, 32, s)
+
+
+def test_gemm_i8_forms_on_two_streams(wr):
+    """Products of every form (whole tiles by pairs, tiles shared by clusters, single CTAs) issued on two
+    streams at once, so that their CTAs share SMs: all of them end, with the results of one stream."""
+    torch = torch_mod()
+    shapes = [(256, 19456, 640), (16, 640, 4096), (300, 2560, 2560), (64, 2560, 9728), (1024, 2560, 512), (9, 300, 128), (2, 512, 300),
+              (333, 2560, 4096), (40, 6144, 640)]
+    cases = []
+    for i, (M, N, K) in enumerate(shapes):
+        x, w, xs, ws = _i8_case(M, N, K, 70 + i)
+        xv, wv = _rows(x, _pad16(K), extra=0)[1], _rows(w, _pad16(K), extra=0)[1]
+        ys = [torch.empty(M, N, device="cuda") for _ in range(3)]
+        cases.append((M, N, K, xv, xs, wv, ws, ys, _i8_workspace(wr, M, N, K)))
+
+    def run(c, slot, stream=None):
+        M, N, K, xv, xs, wv, ws, ys, (space, nb) = c
+        wr.wr_gemm_i8(M, N, K, xv, _pad16(K), xs, wv, _pad16(K), ws, wr.WR_F32, ys[slot], N, space, nb, stream=stream)
+
+    for c in cases:
+        run(c, 2)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(40):
+        for k in range(len(cases)):
+            run(cases[k], 0, streams[0])
+            run(cases[(5 * k + rep) % len(cases)], 1, streams[1])
+    torch.cuda.synchronize()
+    for c in cases:
+        assert torch.equal(c[7][0], c[7][2]) and torch.equal(c[7][1], c[7][2])
+    assert wr.wr_get_device_error() == 0

@@ -72,7 +72,7 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
 // steps in flight; x comes from L1. Memory latency is what a matrix of this size is bound by, so share is
 // what lets a warp have all of its bytes on their way at once (up to K = 16384). Where there are rows for more
 // than two rounds of CTAs, a CTA takes rows in turn (19456 rows of 2560: 9.2 us, a CTA for every four rows
-// 10.0; 6144 rows: 4.6 and 3.7).
+// 10.0; 6144 rows: 4.6 and 4.3).
 constexpr int kGemvThreads = 128, kGemvCtas = 148 * 9;   // nine CTAs fill an SM's registers
 template <int MT>
 __global__ void __launch_bounds__(kGemvThreads, 9) gemv_i8_kernel(const GemmI8Args a, const int share) {
@@ -616,29 +616,29 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool>* done) {
   return cudaSuccess;
 }
 
-// Expected time of a plan in microseconds. The form follows the machine (bytes into an SM, clocks of the
-// tensor core, memory, a start and an end for each tile); the constants are fitted to the times of all
-// plans on 216 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). On 96 other shapes the plan it picked took
-// 3 % longer than the best one in the geometric mean, and one CTA a tile with the fewest token tiles and
-// K whole 47 %.
+// Expected time of a plan in microseconds, in a stream of such calls. The form follows the machine (bytes into
+// an SM, clocks of the tensor core, memory, a start and an end for each tile); the constants are fitted to the
+// times of all plans on 175 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). On 63 other shapes the plan
+// it picked took 1 %% longer than the best one in the geometric mean, and one CTA a tile with the fewest
+// token tiles and K whole 46 %%.
 double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
   const int cg = 1 + p.pair, tn = p.tn;
-  // weights that several token tiles read are read once more now and then
-  const double memory = (1.36 * (p.mt > 1 ? 1.0 : 1 / 1.36) * N * K + M * K + 2.0 * M * N) / 5.5e6;
+  // weights that several token tiles read come from memory more than once now and then
+  const double memory = ((p.mt > 1 ? 1.35 : 1.0) * N * K + M * K + 2.0 * M * N) / 6.0e6;
   const double tensor = 2.0 * tn / 1900;                           // one block: 8192 products a clock
   if (p.persistent) {
     const int64_t rounds = (p.tiles + kSMs / 2 - 1) / (kSMs / 2);
-    const double block = std::max(tensor, (16384 + 64.0 * tn) / 100e3);
-    return 3.9 + std::max(rounds * std::max(p.kb * block, 0.021 * tn), memory) + 0.010 * tn;
+    const double block = std::max(tensor, (16384 + 64.0 * tn) / 101e3);
+    return 3.0 + std::max(rounds * std::max(p.kb * block, 0.024 * tn), memory) + 0.009 * tn;
   }
   // two CTAs on their own share an SM; clusters run at once
   const bool alone = p.tiles <= kClusters[cg * p.split];
   const int64_t waves = alone ? 1 : (p.tiles + 2 * kSMs - 1) / (2 * kSMs), even = (p.tiles + kSMs - 1) / kSMs;
   const int64_t most = alone ? 1 : std::max(2 * waves - 1, std::min(2 * waves, even));   // CTAs of the busiest SM
   const int blocks = (p.kb + p.split - 1) / p.split;
-  const double block = std::max(tensor, (16384 + 128.0 * tn / cg) / 118e3);
-  double t = 1.3 + 0.13 * p.pair + std::max(most * blocks * block, memory) + waves * 2.1;
-  t += p.split > 1 ? 0.5 + 0.02 * cg * cg * p.split * p.split + waves * 0.025 * tn : waves * 0.023 * tn;
+  const double block = std::max(tensor, (16384 + 128.0 * tn / cg) / 124e3);
+  double t = 0.3 + 0.39 * p.pair + std::max(most * blocks * block, memory) + waves * 2.2;
+  t += p.split > 1 ? 0.64 + 0.014 * cg * cg * p.split * p.split + waves * 0.023 * tn : waves * 0.022 * tn;
   return t;
 }
 

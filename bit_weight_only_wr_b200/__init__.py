@@ -1,4 +1,4 @@
-"""Python binding of libwr (packed low-bit weight-only GEMV/GEMM for B200).
+"""Python binding of libwr (packed low-bit weight-only GEMV/GEMM for B200, and the 8-bit token path).
 
 Argument marshalling only: every function forwards to the C entry point of the same name in
 ``libwr.so`` (declared in ``include/wr.h``). Device operands are torch CUDA tensors (or raw

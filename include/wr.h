@@ -334,8 +334,8 @@ wr_status wr_gemv_ternary_batched(int64_t M, int32_t count, const wr_gemv_ternar
  * either those or the 8-bit tokens of wr_gemm_i8. No counterpart in the pages.
  *
  * Element types of these calls. Strides (ld*) are in elements, from one row to the next; a row's
- * elements are contiguous. Nothing between two rows is read or written, nor anything behind the last
- * element of the last row. Base pointers are 16-byte aligned as everywhere; rows that all start on 16
+ * elements are contiguous. What stands between two rows or behind the last one is neither used nor
+ * written. Base pointers are 16-byte aligned as everywhere; rows that all start on 16
  * bytes are moved in 16-byte pieces, others element by element (slower). Outputs must not overlap
  * inputs except where stated. */
 enum { WR_F32 = 0, WR_BF16 = 1, WR_F16 = 2, WR_I8 = 3 };
@@ -360,8 +360,9 @@ wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_
  * x_scale fp32 [M], w_scale fp32 [N], bias fp32 [N] or null; y of y_type WR_F32, WR_BF16 or WR_F16
  * (ldy >= N). The sums are exact integers; the fp32 conversion, the two products (x_scale first) and
  * the bias round once each, then the type of y does: the result is the same bits on every run and for
- * every M. The workspace rules are those of the other calls (a size of 0 means that none is needed;
- * the pointer may then be null). */
+ * every M. The workspace rules are those of the other calls; at present no size needs one: the size is 0
+ * and the pointer may be null. One or two tokens run on integer dot products, more on tcgen05 (kind::i8)
+ * with the tile, the split of K and the form chosen by the expected time. */
 size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
                      const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,

@@ -682,3 +682,89 @@ def test_gemm_i8_forms_on_two_streams(wr):
     for c in cases:
         assert torch.equal(c[7][0], c[7][2]) and torch.equal(c[7][1], c[7][2])
     assert wr.wr_get_device_error() == 0
+
+
+def _chain(wr, M, steps, sync, graph=False):
+    """A run in which every call reads what the call before it wrote, products behind products among them:
+    codes of h, a product, its first row as the bias of another, and norms in place."""
+    torch = torch_mod()
+    H = 640
+    g = _gen(7)
+    h = torch.randn(M, H, device="cuda", generator=g)
+    h0 = h.clone()
+    W = torch.randint(-127, 128, (H, H), device="cuda", generator=g, dtype=torch.int32).to(torch.int8)
+    ws = torch.full((H,), 1e-4, device="cuda")
+    wn = torch.ones(H, device="cuda")
+    q, s = torch.empty(M, H, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    y, z = torch.empty(M, H, device="cuda"), torch.empty(M, H, device="cuda")
+    space, nb = _i8_workspace(wr, M, H, H)
+
+    def step():
+        wr.wr_quantize_rows(wr.WR_F32, M, H, h, H, q, H, s)
+        sync()
+        wr.wr_gemm_i8(M, H, H, q, H, s, W, H, ws, wr.WR_F32, y, H, space, nb)
+        sync()
+        wr.wr_gemm_i8(M, H, H, q, H, s, W, H, ws, wr.WR_F32, z, H, space, nb, bias=y)
+        sync()
+        wr.wr_gemm_i8(M, H, H, q, H, s, W, H, ws, wr.WR_F32, y, H, space, nb, bias=z)
+        sync()
+        wr.wr_residual_norm(M, H, block=y, ld_block=H, residual=h, ld_residual=H, residual_out=h, ld_residual_out=H, norm_weight=wn,
+                            y=z, ld_y=H, residual_scale=0.5)
+        sync()
+        wr.wr_residual_norm(M, H, block=z, ld_block=H, residual=h, ld_residual=H, residual_out=h, ld_residual_out=H, residual_scale=0.5)
+        sync()
+
+    if graph:
+        step()
+        torch.cuda.synchronize()
+        h.copy_(h0)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            step()
+        h.copy_(h0)
+        for _ in range(steps):
+            gr.replay()
+    else:
+        for _ in range(steps):
+            step()
+    torch.cuda.synchronize()
+    return h.clone(), y.clone(), z.clone()
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 40, 300, 1500])
+def test_calls_that_follow_one_another(wr, M):
+    """The products start before the call in front of them has ended: with nothing between the calls, in a graph,
+    and with a wait after each call the results are the same bits."""
+    torch = torch_mod()
+    waited = _chain(wr, M, 12, torch.cuda.synchronize)
+    for got in (_chain(wr, M, 12, lambda: None), _chain(wr, M, 12, lambda: None, graph=True)):
+        assert all(torch.equal(a, b) for a, b in zip(got, waited))
+    assert bool(torch.isfinite(waited[0]).all()) and wr.wr_get_device_error() == 0
+
+
+def test_many_short_rows(wr):
+    torch = torch_mod()
+    for M, K in ((100001, 24), (70000, 3)):
+        x = torch.randn(M, K, device="cuda", generator=_gen(M))
+        q, s = _quantize(wr, x)
+        qr, sr = _codes64(x.cpu().numpy())
+        assert np.array_equal(q.cpu().numpy(), qr) and np.array_equal(s.cpu().numpy(), sr)
+        _norm_check(wr, _norm_case(M, K, gate="row"), M, K, "i8")
+
+
+@pytest.mark.parametrize("M,D", [(2, 12000), (3, 20000), (700, 9000), (400, 17000)])
+def test_norm_long_rows_in_place(wr, M, D):
+    _norm_check(wr, _norm_case(M, D, gate="token"), M, D, "bf16", in_place=True, pad=8)
+    _norm_check(wr, _norm_case(M, D, "f32", "f32", gdt="f32", weights="f32"), M, D, "i8", in_place=True, rdt="f32", bdt="f32", wdt="f32", pad=1)
+
+
+def test_tensors_of_another_device_are_refused(wr):
+    class Other:   # what the binding asks of a tensor
+        def get_device(self):
+            return 1 + torch_mod().cuda.current_device()
+
+        def data_ptr(self):
+            return 1 << 20
+
+    with pytest.raises(ValueError, match="current device"):
+        wr.wr_quantize_rows(wr.WR_F32, 2, 32, Other(), 32, 1 << 20, 32, 1 << 20)

@@ -93,3 +93,33 @@ def test_host_tensors_are_refused():
     import torch
     with pytest.raises(ValueError):
         wr.wr_quantize_rows(wr.WR_F32, 2, 16, torch.zeros(2, 16), 16, P, 16, P, stream=0)
+
+
+def test_arguments_by_name_and_by_place():
+    """The extension module takes arguments as a Python function does."""
+    with pytest.raises(TypeError, match="missing"):
+        wr.wr_quantize_rows(wr.WR_F32, 2, 16)
+    with pytest.raises(TypeError, match="unexpected"):
+        wr.wr_quantize_rows(**QUANT, stream=0, colour=3)
+    with pytest.raises(TypeError, match="multiple"):
+        wr.wr_quantize_rows(wr.WR_F32, **QUANT, stream=0)
+    with pytest.raises(TypeError, match="positional"):
+        wr.wr_residual_norm(1, 2, 3)
+    with pytest.raises(TypeError):
+        wr.wr_quantize_rows(**{**QUANT, "M": "4"}, stream=0)
+    with pytest.raises(OverflowError):
+        wr.wr_quantize_rows(**{**QUANT, "type": 1 << 40}, stream=0)
+    name = "".join(["l", "dx"])   # an equal string that is not the interned one
+    assert _status(wr.wr_quantize_rows, **{**{k: v for k, v in QUANT.items() if k != "ldx"}, name: 99}) == BAD
+    q = dict(QUANT)
+    place = [q.pop(k) for k in ("type", "M", "K", "x", "ldx")]
+    assert _status(wr.wr_quantize_rows, *place[:-1], 99, **q) == BAD
+
+
+def test_the_message_of_a_refusal():
+    e = None
+    try:
+        wr.wr_gemm_i8(**{**GEMM, "M": 0}, stream=0)
+    except wr.WrError as err:
+        e = err
+    assert e is not None and e.status == BAD and str(e) == "wr_gemm_i8: invalid argument (status 1)"

@@ -9,7 +9,6 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.cuh"
 #include "i8_kernels.cuh"
 #include "tc_common.cuh"
 #include "tc_kernels.cuh"

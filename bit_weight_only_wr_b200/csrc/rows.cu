@@ -388,6 +388,34 @@ __global__ void __launch_bounds__(MAXT) quantize_rows_kernel(const QuantRowsArgs
 
 // ---------------------------------------------------------------- residual + norm
 
+template <int VPT>
+__device__ __forceinline__ f32x2 squares(const Vec8 (&v)[VPT], f32x2 scale) {
+  f32x2 ss = splat2(0.f);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x2 x = mul2(v[i].p[j], scale);
+      ss = fma2(x, x, ss);
+    }
+  return ss;
+}
+// 1 / sqrt(mean of squares + eps) of a row. Where the sum leaves fp32's range (values beyond 2^56, or below
+// 2^-50 with nothing to speak of added) the squares are summed again of values scaled by a power of two: a
+// row of numbers of that size is normed like any other.
+template <int VPT>
+__device__ __forceinline__ float inv_rms(const Vec8 (&v)[VPT], float inv_d, float eps, float* buf, float* buf2) {
+  f32x2 s2 = splat2(0.f);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s2 = fma2(v[i].p[j], v[i].p[j], s2);
+  const float ss = row_sum(s2, buf);
+  if (ss <= 3.4e38f && (ss >= 1e-30f || eps >= 1e-30f)) return rsqrtf(ss * inv_d + eps);
+  const float s = ss < 1.f ? 0x1p+80f : 0x1p-80f;
+  return s * rsqrtf(row_sum(squares(v, splat2(s)), buf2) * inv_d + eps * s * s);
+}
+
 // B32, R32, W32: whether the block, the residual, and the weights (the gate is usually like them) are fp32.
 struct NormArgs {
   wr_residual_norm_args p;
@@ -398,6 +426,7 @@ template <int VPT, int MAXT, bool VEC, bool B32, bool R32, bool W32>
 __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) {
   const wr_residual_norm_args& a = na.p;
   __shared__ float buf_post[32], buf_norm[32];
+  __shared__ float wide_post[32], wide_norm[32];
   __shared__ uint32_t buf_max[32];
   const int T = blockDim.x, t = threadIdx.x, D = (int)a.D;
   const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -442,16 +471,10 @@ __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) 
       for (int j = 0; j < 4; ++j) v[i].p[j] = splat2(0.f);
   }
   if (a.post_norm) {
-    f32x2 ss = splat2(0.f);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ss = fma2(v[i].p[j], v[i].p[j], ss);
-    const float r = rsqrtf(row_sum(ss, buf_post) * na.inv_d + a.eps);
+    const float r = inv_rms<VPT>(v, na.inv_d, a.eps, buf_post, wide_post);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) scale8(v[i], r, pw, rp[i]);
   }
-  f32x2 ss = splat2(0.f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     if (a.gate) {
@@ -465,8 +488,6 @@ __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) 
       for (int j = 0; j < 4; ++j) v[i].p[j] = fma2(rs, w.p[j], v[i].p[j]);
     }
     if (nw) rn[i] = load8<W32, VEC>(nw, i, T, t, D);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) ss = fma2(v[i].p[j], v[i].p[j], ss);
   }
   if (a.residual_out) {
     uint8_t* o = static_cast<uint8_t*>(a.residual_out) + m * a.ld_residual_out * (R32 ? 4 : 2);
@@ -474,7 +495,7 @@ __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const NormArgs na) 
     for (int i = 0; i < VPT; ++i) store8<VEC>(o, a.residual_type, i, T, t, D, v[i]);
   }
   if (!a.y) return;
-  const float r = rsqrtf(row_sum(ss, buf_norm) * na.inv_d + a.eps);
+  const float r = inv_rms<VPT>(v, na.inv_d, a.eps, buf_norm, wide_norm);
   uint8_t* y = static_cast<uint8_t*>(a.y) + m * a.ld_y * type_bytes(a.y_type);
   float amax = 0.f;
 #pragma unroll

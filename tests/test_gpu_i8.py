@@ -768,3 +768,62 @@ def test_tensors_of_another_device_are_refused(wr):
 
     with pytest.raises(ValueError, match="current device"):
         wr.wr_quantize_rows(wr.WR_F32, 2, 32, Other(), 32, 1 << 20, 32, 1 << 20)
+
+
+@pytest.mark.parametrize("D", [7, 300, 2560, 9000, 20000])
+@pytest.mark.parametrize("M", [2, 400])
+def test_norm_of_very_large_and_very_small_rows(wr, M, D):
+    """Rows whose squares leave fp32's range are normed like any other (rows of ordinary size beside them)."""
+    torch = torch_mod()
+    for size, eps in ((1e25, 1e-6), (3e37, 0.0), (1e-22, 0.0), (1e-30, 0.0)):
+        c = _norm_case(M, D, "f32", "f32")
+        for k in ("b", "h"):
+            c[k][0] *= size / 8
+        c["b"][1] *= size / 8   # the block alone: the post-norm brings it back
+        _norm_check(wr, c, M, D, "f32", rdt="f32", bdt="f32", eps=eps)
+        h = torch.zeros(M, D, device="cuda")
+        h[0], h[1] = c["h"][0], 1.0
+        y = torch.empty(M, D, device="cuda")
+        wr.wr_residual_norm(M, D, residual=h, ld_residual=D, y=y, ld_y=D, eps=eps)
+        v = h[:2].double()
+        ref = v / torch.sqrt((v * v).mean(1, keepdim=True) + eps)
+        assert bool(((y[:2].double() - ref).abs() <= 33 * U * ref.abs()).all())
+
+
+def test_two_host_threads(wr):
+    """Two threads that call at once, each on its own stream with its own tensors."""
+    import threading
+    torch = torch_mod()
+    shapes = [(3, 640, 2560), (300, 512, 1024)]
+    work = []
+    for i, (M, N, K) in enumerate(shapes):
+        x, w, xs, ws = _i8_case(M, N, K, 90 + i)
+        h = torch.randn(M, K, device="cuda", generator=_gen(i))
+        work.append((M, N, K, h, w, ws, torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"),
+                     [torch.empty(M, N, device="cuda") for _ in range(2)], torch.cuda.Stream()))
+    errors = []
+
+    def run(i, slot, stream, times):
+        M, N, K, h, w, ws, q, s, ys, _ = work[i]
+        for _ in range(times):
+            wr.wr_quantize_rows(wr.WR_F32, M, K, h, K, q, K, s, stream=stream)
+            wr.wr_gemm_i8(M, N, K, q, K, s, w, K, ws, wr.WR_F32, ys[slot], N, None, 0, stream=stream)
+
+    def thread(i):
+        try:
+            run(i, 0, work[i][9], 200)
+        except Exception as e:   # seen by the main thread below
+            errors.append(e)
+
+    for i in range(2):
+        run(i, 1, None, 1)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for i in range(2):
+        assert torch.equal(work[i][8][0], work[i][8][1])

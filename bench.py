@@ -806,6 +806,62 @@ def run_extras(args, wr, torch, np, stream, dist, hbm_peak, bf16_peak):
         out["ternary"] = res
     except Exception as e:  # noqa: BLE001
         out["ternary"] = {"error": repr(e)}
+
+    # the same body at 8 bits (random int8 weights of its shapes), layer by layer with its norms and the
+    # codes of each linear's input; the attention output is a stand-in
+    try:
+        out["eight_bit"] = eight_bit_body(args, wr, torch, stream, hbm_peak, bf16_peak)
+    except Exception as e:  # noqa: BLE001
+        out["eight_bit"] = {"error": repr(e)}
+    return out
+
+
+def eight_bit_body(args, wr, torch, stream, hbm_peak, bf16_peak):
+    """A decoder body whose linears are all at 8 bits, as dependent calls in one graph. Per layer: norm to
+    codes, stacked q/k/v; codes of the attention output, o; residual and norm to codes, stacked gate/up; codes
+    of silu(gate) up, down; the next layer's first norm takes down's output."""
+    H, QKV, A, F = 2560, 6144, 4096, 9728
+    g = torch.Generator(device="cuda").manual_seed(11)
+    layers = []
+    for _ in range(args.layers):
+        layers.append([(torch.randint(-127, 128, (n, k), device="cuda", generator=g, dtype=torch.int8),
+                        torch.full((n,), 1e-3 / k ** 0.5, device="cuda"), n, k)
+                       for n, k in ((QKV, H), (H, A), (2 * F, H), (H, F))])
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    out = {}
+    for M in (1, 8, 512):
+        h, att = torch.randn(M, H, device="cuda", generator=g).bfloat16(), torch.randn(M, A, device="cuda", generator=g).bfloat16()
+        q = {k: torch.empty(M, k, dtype=torch.int8, device="cuda") for k in (H, A, F)}
+        s = {k: torch.empty(M, device="cuda") for k in (H, A, F)}
+        y = {n: torch.empty(M, n, dtype=torch.bfloat16, device="cuda") for n in (QKV, 2 * F)}
+        d = torch.empty(M, H, device="cuda")
+
+        def linear(item, x, xs, yt, yo):
+            wq, ws, n, k = item
+            wr.wr_gemm_i8(M, n, k, x, k, xs, wq, k, ws, yt, yo, n, None, 0)
+
+        def norm(block):
+            wr.wr_residual_norm(M, H, block=block, ld_block=H, residual=h, ld_residual=H, residual_out=h, ld_residual_out=H,
+                                residual_type=wr.WR_BF16, norm_weight=w, weight_type=wr.WR_BF16, y=q[H], ld_y=H,
+                                y_type=wr.WR_I8, y_scale=s[H])
+
+        def step():
+            for i, (qkv, o, gate_up, down) in enumerate(layers):
+                norm(d if i else None)
+                linear(qkv, q[H], s[H], wr.WR_BF16, y[QKV])
+                wr.wr_quantize_rows(wr.WR_BF16, M, A, att, A, q[A], A, s[A])
+                linear(o, q[A], s[A], wr.WR_F32, d)
+                norm(d)
+                linear(gate_up, q[H], s[H], wr.WR_BF16, y[2 * F])
+                gu = y[2 * F]
+                wr.wr_quantize_rows(wr.WR_BF16, M, F, gu[:, F:], 2 * F, q[F], F, s[F], gate=gu, ldg=2 * F)
+                linear(down, q[F], s[F], wr.WR_F32, d)
+        ms = graph_time_ms(torch, step, 5, 3, stream) / 5
+        weights = sum(n * k for it in layers for _, _, n, k in it)
+        out[f"body_dependent_M{M}"] = {"ms": ms, "weight_bytes": weights, "gbs": weights / ms / 1e6,
+                                       "frac_of_hbm": weights / ms / 1e6 / hbm_peak, "tops": 2 * M * weights / ms / 1e9,
+                                       "frac_of_2x_bf16": 2 * M * weights / ms / 1e9 / (2 * bf16_peak), "tokens_per_s": M * 1e3 / ms,
+                                       "launches": 8 * len(layers)}
     return out
 
 

@@ -382,7 +382,7 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
  * residual (and residual_out), gate and weights each WR_F32, WR_BF16 or WR_F16 (0 where unused).
  * 1 <= D <= 32768 (larger D: WR_ERR_UNSUPPORTED); eps >= 0, all three floats finite. A row of zeros
  * needs eps > 0 to stay zero (0 / 0 otherwise). Squares are summed in fp32, of scaled values where the sum
- * would leave its range. */
+ * would leave its range (a row of subnormal numbers with eps = 0 has no finite reciprocal all the same). */
 typedef struct {
   int64_t M, D;
   const void *block, *residual, *gate;

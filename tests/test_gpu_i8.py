@@ -827,3 +827,62 @@ def test_two_host_threads(wr):
     assert not errors
     for i in range(2):
         assert torch.equal(work[i][8][0], work[i][8][1])
+
+
+def test_products_behind_copies_fills_and_other_streams(wr):
+    """A product captured (and issued) right behind a fill, a copy, a torch kernel, an event of another stream:
+    what is in front of it in the stream need not be one of this library's kernels."""
+    torch = torch_mod()
+    for M in (1, 40, 1500):
+        N, K = 512, 640
+        x, w, xs, ws = _i8_case(M, N, K, M)
+        want = _i8_check(wr, x, w, xs, ws).clone()
+        xq, y, other = torch.empty_like(x), torch.empty(M, N, device="cuda"), torch.cuda.Stream()
+        host = x.cpu().pin_memory()
+
+        def product():
+            wr.wr_gemm_i8(M, N, K, xq, K, xs, w, K, ws, wr.WR_F32, y, N, None, 0)
+
+        def behind_fill():
+            xq.copy_(x)
+            y.zero_()          # a memset
+            product()
+
+        def behind_copy():
+            xq.copy_(x)        # device to device
+            product()
+
+        def behind_upload():
+            xq.copy_(host, non_blocking=True)
+            product()
+
+        def behind_kernel():
+            torch.neg(x, out=xq)
+            torch.neg(xq, out=xq)   # (-128 is its own negative: twice is the identity)
+            product()
+
+        def behind_event():
+            cur = torch.cuda.current_stream()
+            other.wait_stream(cur)
+            with torch.cuda.stream(other):
+                xq.copy_(x)
+                y.zero_()
+            cur.wait_stream(other)
+            product()
+
+        for f in (behind_fill, behind_copy, behind_upload, behind_kernel, behind_event):
+            for _ in range(3):
+                xq.zero_()
+                f()
+                torch.cuda.synchronize()
+                assert torch.equal(y, want)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                f()
+                product()
+            for _ in range(3):
+                xq.zero_()
+                y.zero_()
+                graph.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(y, want)

@@ -702,9 +702,9 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
   if (!aligned16(x) || !aligned16(x_scale) || !aligned16(w) || !aligned16(w_scale) || (bias && !aligned16(bias)) ||
       !aligned16(y))
     return WR_ERR_INVALID_ARG;
-  const bool few = wr::gemv_i8_pays(M, N, K);
+  const wr::I8Kernel kernel = wr::gemm_i8_kernel_for(M, N, K);
   wr::GemmI8Plan plan{};
-  if (!few && !wr::plan_gemm_i8(M, N, K, &plan)) return WR_ERR_INVALID_ARG;
+  if (kernel == wr::I8Kernel::kTcgen05 && !wr::plan_gemm_i8(M, N, K, &plan)) return WR_ERR_INVALID_ARG;
   (void)workspace;
   (void)workspace_bytes;
   wr::GemmI8Args a{};
@@ -722,7 +722,9 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
   a.K = (int)K;
   a.y_type = y_type;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = few ? wr::launch_gemv_i8(a, s) : wr::launch_gemm_i8(a, plan, device_error_word(), s);
+  const cudaError_t e = kernel == wr::I8Kernel::kDp4a  ? wr::launch_gemv_i8(a, s)
+                        : kernel == wr::I8Kernel::kFew ? wr::launch_few_i8(a, s)
+                                                       : wr::launch_gemm_i8(a, plan, device_error_word(), s);
   return e == cudaSuccess ? WR_OK : WR_ERR_CUDA;
 }
 

@@ -147,6 +147,113 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
   return launch_overlapped(gemv_i8_kernel<MT>, dim3((unsigned)grid), dim3(kGemvThreads), 0, 1, stream, a, share);
 }
 
+// ---------------------------------------------------------------- up to 16 tokens: mma.sync, one pass over w
+
+// Few tokens are bound by the latency of the rows, not by products, and a tile on tcgen05 has a start and an end
+// of 2 us. Here a CTA owns 16 rows of w (the m of mma.m16n8k32) and NT times 8 tokens (its n); its eight warps
+// take turns of 128 bytes of K, U turns at once, and add up in shared memory. The order of K inside an MMA is
+// free as long as both operands keep it: lane 4 g + t loads 32 contiguous bytes of rows g and g + 8 and of
+// tokens g, g + 8, so that rows come in whole 128-byte lines straight into the registers that the MMAs take.
+// 8 tokens of 2560 x 4096 3.8 us (tcgen05 5.2), 4096 x 2560 3.8 (4.9), 6144 x 2560 4.2 (6.2); the last bytes of
+// rows stand outside the loop (inside it: 4.5, 2560 x 4096). A ring of bulk copies in its place: 6.3.
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
+__device__ __forceinline__ void mma_i8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int U, int CTAS, int NT>
+__global__ void __launch_bounds__(kFewThreads, CTAS) few_i8_kernel(const GemmI8Args a) {
+  __shared__ int parts[kFewWarps][8 * NT][17];   // [warp][token][row]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  const int whole = a.K / 16, rest = a.K % 16;   // 16-byte pieces of a row
+  grid_launch_dependents();
+  // the rows may come to L2 while the kernel before this one still runs
+  {
+    const int lines = (a.K + 127) / 128, row = threadIdx.x & 15;
+    if (n0 + row < a.N)
+      for (int l = threadIdx.x >> 4; l < lines; l += kFewThreads / 16) prefetch_l2(a.w + (int64_t)(n0 + row) * a.ldw + l * 128);
+  }
+  grid_dependency_wait();
+  const bool real0 = n0 + g < a.N, real1 = n0 + g + 8 < a.N;
+  const int8_t* w0 = a.w + (int64_t)(real0 ? n0 + g : 0) * a.ldw;
+  const int8_t* w1 = a.w + (int64_t)(real1 ? n0 + g + 8 : 0) * a.ldw;
+  const int8_t* x[NT];
+  bool realx[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    realx[j] = g + 8 * j < a.M;
+    x[j] = a.x + (int64_t)(realx[j] ? g + 8 * j : 0) * a.ldx;
+  }
+  int c[NT][4] = {};
+  const int full = a.K / 128, steps = (a.K + 127) / 128;   // turns of 128 bytes: whole ones, all
+  for (int s0 = warp; s0 < full; s0 += kFewWarps * U) {
+    uint4 p0[U][2], p1[U][2], px[U][2][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int s = s0 + kFewWarps * u, k = s * 8 + 2 * t + h;   // 16-byte piece
+        p0[u][h] = chunk_if<false>(w0 + 16 * k, s < full && real0);
+        p1[u][h] = chunk_if<false>(w1 + 16 * k, s < full && real1);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int s = s0 + kFewWarps * u, k = s * 8 + 2 * t + h;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) px[u][h][j] = chunk_if<true>(x[j] + 16 * k, s < full && realx[j]);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_i8(c[j], p0[u][h].x, p1[u][h].x, p0[u][h].y, p1[u][h].y, px[u][h][j].x, px[u][h][j].y);
+          mma_i8(c[j], p0[u][h].z, p1[u][h].z, p0[u][h].w, p1[u][h].w, px[u][h][j].z, px[u][h][j].w);
+        }
+      }
+  }
+  if (full < steps && warp == full % kFewWarps) {   // the rows' last bytes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = full * 8 + 2 * t + h;
+      uint4 p0 = chunk_if<false>(w0 + 16 * k, k < whole && real0), p1 = chunk_if<false>(w1 + 16 * k, k < whole && real1);
+      if (rest != 0 && k == whole) {
+        if (real0) p0 = row_end(w0 + 16 * k, rest);
+        if (real1) p1 = row_end(w1 + 16 * k, rest);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint4 px = chunk_if<true>(x[j] + 16 * k, k < whole && realx[j]);
+        if (rest != 0 && k == whole && realx[j]) px = row_end(x[j] + 16 * k, rest);
+        mma_i8(c[j], p0.x, p1.x, p0.y, p1.y, px.x, px.y);
+        mma_i8(c[j], p0.z, p1.z, p0.w, p1.w, px.z, px.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    parts[warp][8 * j + 2 * t][g] = c[j][0];
+    parts[warp][8 * j + 2 * t + 1][g] = c[j][1];
+    parts[warp][8 * j + 2 * t][g + 8] = c[j][2];
+    parts[warp][8 * j + 2 * t + 1][g + 8] = c[j][3];
+  }
+  const int n = n0 + (threadIdx.x & 15);
+  const float ws = n < a.N ? a.w_scale[n] : 0.f;
+  __syncthreads();
+  for (int m = threadIdx.x >> 4; m < a.M; m += kFewThreads / 16) {
+    if (n >= a.N) break;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kFewWarps; ++i) sum += parts[i][m][threadIdx.x & 15];
+    store_y(a.y, a.y_type, m * a.ldy + n, scaled(sum, a.x_scale[m], ws, a.bias, n));
+  }
+}
+
 // ---------------------------------------------------------------- more tokens: tcgen05 kind::i8
 
 // The channels are the rows of the MMA (A, 128 a CTA), the tokens its columns (B), so that a thread of the
@@ -710,6 +817,13 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {
   return a.M == 1 ? run_gemv<1>(a, stream) : run_gemv<2>(a, stream);
+}
+
+cudaError_t launch_few_i8(const GemmI8Args& a, cudaStream_t stream) {
+  // four turns at once where K has them for all warps, else two and a third CTA on the SM (8 tokens of
+  // 2560 x 4096: 3.8 and 4.4 us; of 6144 x 2560: 4.9 and 4.0)
+  const auto kern = a.M > 8 ? few_i8_kernel<2, 2, 2> : a.K >= 4096 ? few_i8_kernel<4, 2, 1> : few_i8_kernel<2, 3, 1>;
+  return launch_overlapped(kern, dim3((unsigned)((a.N + 15) / 16)), dim3(kFewThreads), 0, 1, stream, a);
 }
 
 }  // namespace wr

@@ -72,11 +72,19 @@ struct GemmI8Plan {
   int tiles;
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
-// One or two tokens run on dp4a where rows are few or long (2560 rows of 4096: 2.7 us a call, on the tensor cores
-// 5.1); many short rows cost it more than a tile does (16384 rows of 1024: 6.7 and 5.2 us, 8192 of 2048: 4.6
-// and 5.8).
-inline bool gemv_i8_pays(int64_t M, int64_t N, int64_t K) { return M <= 2 && (K > 1024 || N <= 4096); }
-cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);
+// The kernel of a call. Measured in a graph of such calls, us (dp4a, warps' MMA, tcgen05):
+//   one token   1024 x 4096: 2.1, 2.6, 4.6;  2560 x 4096: 2.7, 4.0, 5.1;  6144 x 1024: 3.7, 2.6, 3.9
+//   8 tokens    2560 x 4096: -, 3.8, 5.2;    8192 x 4096: -, 8.0, 8.7;    6144 x 9728: -, 15.8, 13.2
+//   16 tokens   4096 x 4096: -, 4.9, 6.6;    6144 x 2560: -, 6.9, 6.0
+enum class I8Kernel { kDp4a, kFew, kTcgen05 };
+inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
+  if (M <= 2 && (K > 1024 || N <= 1024)) return I8Kernel::kDp4a;
+  if (M <= 8 && (N <= 4096 || (N <= 8192 && K <= 4096))) return I8Kernel::kFew;
+  if (M <= 16 && N <= 4096 && K <= 4096) return I8Kernel::kFew;
+  return I8Kernel::kTcgen05;
+}
+cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);   // M <= 2
+cudaError_t launch_few_i8(const GemmI8Args& a, cudaStream_t stream);    // M <= 16
 cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream);
 // Sums of K products of int8 values stay inside int32 up to this K ((-128)^2 * K < 2^31).
 constexpr int64_t kMaxI8K = 131071;

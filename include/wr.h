@@ -361,8 +361,9 @@ wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_
  * (ldy >= N). The sums are exact integers; the fp32 conversion, the two products (x_scale first) and
  * the bias round once each, then the type of y does: the result is the same bits on every run and for
  * every M. The workspace rules are those of the other calls; at present no size needs one: the size is 0
- * and the pointer may be null. One or two tokens run on integer dot products, more on tcgen05 (kind::i8)
- * with the tile, the split of K and the form chosen by the expected time. */
+ * and the pointer may be null. Up to 16 tokens of matrices that are not too large run on kernels that
+ * pass over w once by warps, all else on tcgen05 (kind::i8) with the tile, the split of K and the form
+ * chosen by the expected time. */
 size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
                      const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,

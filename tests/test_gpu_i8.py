@@ -886,3 +886,13 @@ def test_products_behind_copies_fills_and_other_streams(wr):
                 graph.replay()
                 torch.cuda.synchronize()
                 assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 9, 16, 17])
+@pytest.mark.parametrize("N,K", [(1024, 1024), (1025, 1025), (4096, 1000), (4097, 4096), (4096, 4097), (4111, 300), (8192, 4096),
+                                 (8193, 513), (12300, 260), (2561, 4100), (40, 20000)])
+def test_gemm_i8_where_the_kernel_changes(wr, M, N, K):
+    """Both sides of the sizes at which another kernel takes over, in every type."""
+    x, w, xs, ws = _i8_case(M, N, K, M + 2 * N + K)
+    for ydt in ("f32", "bf16", "f16"):
+        _i8_check(wr, x, w, xs, ws, ydt, ldy=N + (M % 2))

@@ -281,7 +281,8 @@ struct GemmBars {
 
 struct GemmParams {
   GemmI8Args a;
-  int tn, mt, kb, tiles, split, stages, tmem_cols;
+  int tn, mt, kb, split, stages, tmem_cols;
+  int whole, cut, cut_tn, units;   // persistent form: see unit_of
   int* err;
 };
 
@@ -322,33 +323,26 @@ __device__ __forceinline__ void drain(GemmBars& bars, const Ring& r, int stages)
   }
 }
 
-// Writes this thread's channel of 16 tokens from token m on (`left` of them real): v plus the bias. A
-// warp holds 32 neighbouring channels, so a token's store is 128 contiguous bytes of fp32. For a
-// 16-bit y neighbouring lanes exchange halves, so that even lanes store pairs of channels of the even
-// tokens and odd lanes those of the odd ones (half the stores; needs rows that start on 4 bytes).
-__device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, int ch, int lane, float v[16], float bias) {
-  if (a.bias) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += bias;
+// y's 16-bit types: one value, and two neighbouring channels.
+struct Bf16Out {
+  static __device__ __forceinline__ uint16_t one(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  if (a.y_type == WR_F32) {
-    if (ch >= a.N) return;
-    float* y = static_cast<float*>(a.y) + (int64_t)m * a.ldy + ch;
-    if (left >= 16) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i * a.ldy] = v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < left) y[i * a.ldy] = v[i];
-    }
-    return;
+};
+struct F16Out {
+  static __device__ __forceinline__ uint16_t one(float v) { return __half_as_ushort(__float2half_rn(v)); }
+  static __device__ __forceinline__ uint32_t two(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  uint32_t h[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    h[i] = a.y_type == WR_BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v[i]))
-                               : (uint32_t)__half_as_ushort(__float2half_rn(v[i]));
+};
+
+// store16 of a 16-bit y: neighbouring lanes exchange values, so that even lanes store pairs of channels of the even
+// tokens and odd lanes those of the odd ones (half the stores and conversions; needs rows that start on 4 bytes).
+template <typename Out>
+__device__ __forceinline__ void store16_half(const GemmI8Args& a, int m, int left, int ch, int lane, const float v[16]) {
   uint16_t* y = static_cast<uint16_t*>(a.y) + (int64_t)m * a.ldy + ch;
   const bool odd = lane & 1;
   if ((a.ldy & 1) == 0 && (ch - lane) + 32 <= a.N && left >= 16) {
@@ -356,15 +350,36 @@ __device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, in
     uint32_t* y2 = reinterpret_cast<uint32_t*>(y - odd) + (odd ? a.ldy / 2 : 0);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[i + 1], 1);
-      y2[(i / 2) * a.ldy] = odd ? (got | h[i + 1] << 16) : (h[i] | got << 16);
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+      y2[(i / 2) * a.ldy] = Out::two(odd ? got : v[i], odd ? v[i + 1] : got);
     }
     return;
   }
   if (ch >= a.N) return;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (i < left) y[i * a.ldy] = (uint16_t)h[i];
+    if (i < left) y[i * a.ldy] = Out::one(v[i]);
+}
+
+// Writes this thread's channel of 16 tokens from token m on (`left` of them real): v plus the bias. A
+// warp holds 32 neighbouring channels, so a token's store is 128 contiguous bytes of fp32.
+__device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, int ch, int lane, float v[16], float bias) {
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += bias;
+  }
+  if (a.y_type == WR_BF16) return store16_half<Bf16Out>(a, m, left, ch, lane, v);
+  if (a.y_type == WR_F16) return store16_half<F16Out>(a, m, left, ch, lane, v);
+  if (ch >= a.N) return;
+  float* y = static_cast<float*>(a.y) + (int64_t)m * a.ldy + ch;
+  if (left >= 16) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i * a.ldy] = v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) y[i * a.ldy] = v[i];
+  }
 }
 
 // 16 tokens of one channel from their sums. xs: their scales (shared memory, readable past `left`).
@@ -453,15 +468,9 @@ __device__ __forceinline__ void exchange(const GemmParams& p, const uint8_t* rin
       } else if (p.a.y_type == WR_F32) {
         *reinterpret_cast<float4*>(static_cast<float*>(p.a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
       } else {
-        uint2 h;
-        if (p.a.y_type == WR_BF16) {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-          h = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        } else {
-          const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
-          h = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.y) + at) = h;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.y) + at) =
+            p.a.y_type == WR_BF16 ? make_uint2(Bf16Out::two(v[0], v[1]), Bf16Out::two(v[2], v[3]))
+                                  : make_uint2(F16Out::two(v[0], v[1]), F16Out::two(v[2], v[3]));
       }
     }
   }
@@ -597,23 +606,47 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   }
 }
 
-// ---- persistent form
+// ---- persistent form. Pairs take tiles in turn. With CUT whole rounds only, and each of the tiles that are left over
+// (fewer than pairs) is cut into `cut` pieces of cut_tn tokens for as many pairs: 256 tokens of 19456 x 2560 are 76
+// tiles for 74 pairs, 19.4 us in two rounds and 16.5 with pieces of 32 tokens (512 tokens 24.6 and 22.7).
+struct Unit {
+  int rg, m0, tn, cols;   // row group, first token, tokens of the MMA, real ones (0 or fewer: nothing to do)
+};
+template <bool CUT>
+__device__ __forceinline__ Unit unit_of(const GemmParams& p, int u) {
+  int t = u, from = 0, tn = p.tn;
+  if (CUT && u >= p.whole) {
+    const int v = u - p.whole;
+    t = p.whole + v / p.cut;
+    from = (v % p.cut) * p.cut_tn;
+    tn = p.cut_tn;
+  }
+  Unit o;
+  o.rg = t / p.mt;
+  o.m0 = (t - o.rg * p.mt) * p.tn + from;
+  o.tn = tn;
+  o.cols = min(CUT ? min(tn, p.tn - from) : tn, p.a.M - o.m0);
+  return o;
+}
+
+template <bool CUT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    gemm_i8_persistent_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+    gemm_i8_persistent_kernel(const GemmParams p, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                              const __grid_constant__ CUtensorMap xmap_cut) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ GemmBars bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int worker = blockIdx.x / 2, G = gridDim.x / 2;
-  const int b_rows = p.tn / 2;                       // tokens that this CTA loads
-  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)b_rows * 128;
+  const uint32_t a_bytes = 128 * 128, stage_bytes = a_bytes + (uint32_t)p.tn / 2 * 128;   // each CTA loads half of the tokens
   volatile int* abort_flag = &bars.abort_flag;
   __shared__ float xs[2][256];
   if (warp == 0) {
     if (lane == 0) {
       prefetch_tensormap(&wmap);
       prefetch_tensormap(&xmap);
+      if (CUT) prefetch_tensormap(&xmap_cut);
     }
     init_bars(bars, p.stages, 2 * kEpilogueThreads / 32);
   }
@@ -629,29 +662,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (lane == 0) {
       Ring r;
       bool ok = true;
-      for (int t = worker; ok && t < p.tiles; t += G) {
-        const int rg = t / p.mt, mt = t - rg * p.mt;
-        const int n0 = (rg * 2 + (int)rank) * 128, m0 = mt * p.tn + (int)rank * b_rows;
+      for (int u = worker; ok && u < p.units; u += G) {
+        const Unit o = unit_of<CUT>(p, u);
+        if (CUT && o.cols <= 0) continue;
+        const int n0 = (o.rg * 2 + (int)rank) * 128, m0 = o.m0 + (int)rank * (o.tn / 2);
+        const CUtensorMap* xm = CUT && u >= p.whole ? &xmap_cut : &xmap;
+        const uint32_t bytes = a_bytes + (uint32_t)o.tn / 2 * 128;
         for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
           if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 511))) break;
           uint8_t* st = ring + r.s * stage_bytes;
           // both CTAs' copies complete on the leader's barrier
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[r.s], 2 * stage_bytes);
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[r.s], 2 * bytes);
           const uint32_t bar = cluster_addr(&bars.full[r.s], 0);
           tma_load_2d_pair(st, &wmap, k * 128, n0, bar);
-          tma_load_2d_pair(st + a_bytes, &xmap, k * 128, m0, bar);
+          tma_load_2d_pair(st + a_bytes, xm, k * 128, m0, bar);
         }
       }
       if (!ok && rank == 0) drain(bars, r, p.stages);
     }
   } else if (warp == 1) {
     if (rank == 0) {   // the leader issues for both CTAs
-      const uint32_t idesc = idesc_i8s(256, p.tn);
       Ring r;
       uint32_t n = 0;
       bool ok = true;
-      for (int t = worker; ok && t < p.tiles; t += G, ++n) {
-        const uint32_t d = n & 1;
+      for (int u = worker; ok && u < p.units; u += G) {
+        const Unit o = unit_of<CUT>(p, u);
+        if (CUT && o.cols <= 0) continue;
+        const uint32_t d = n & 1, idesc = idesc_i8s(256, o.tn);
         if (!(ok = mbar_wait(&bars.acc_empty[d], ((n >> 1) & 1) ^ 1, abort_flag, p.err, 512))) break;
         fence_after_sync();
         for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
@@ -662,19 +699,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                         &bars.empty[r.s], 3);
         }
         if (ok) mma_commit_pair_elect(&bars.acc_full[d], 3);
+        ++n;
       }
     }
   } else {
-    const int q = warp & 3, turn = warp >= 6;
+    // The scales of a tile are read while the one before it is written (8 rounds of 256 x 32 tokens and one block of
+    // K: 9.8 us, read at a tile's start 10.4).
+    const int q = warp & 3, turn = (warp - 2) >> 2, te = threadIdx.x - 64;
+    float ws_next, bias_next, xs_next;
+    auto scales = [&](const Unit& o) {
+      const int ch = (o.rg * 2 + (int)rank) * 128 + 32 * q + lane;
+      ws_next = ch < p.a.N ? p.a.w_scale[ch] : 0.f;
+      bias_next = p.a.bias && ch < p.a.N ? p.a.bias[ch] : 0.f;
+      xs_next = te < o.cols ? p.a.x_scale[o.m0 + te] : 0.f;
+    };
     uint32_t n = 0;
-    for (int t = worker; t < p.tiles; t += G, ++n) {
+    int u = worker;
+    Unit o = unit_of<CUT>(p, u);
+    scales(o);
+    for (; u < p.units; u += G) {
+      const Unit now = o;
+      const float ws = ws_next, bias = bias_next;
       const uint32_t d = n & 1;
-      const int rg = t / p.mt, mt = t - rg * p.mt;
-      const int ch = (rg * 2 + (int)rank) * 128 + 32 * q + lane, m0 = mt * p.tn;
-      const int cols = min(p.tn, p.a.M - m0);         // tokens of this tile
-      const float ws = ch < p.a.N ? p.a.w_scale[ch] : 0.f;
-      const float bias = p.a.bias && ch < p.a.N ? p.a.bias[ch] : 0.f;
-      stage_scales(xs[d], p.a.x_scale + m0, cols, p.tn, threadIdx.x - 64);
+      if (te < 256) xs[d][te] = xs_next;
+      if (u + G < p.units) scales(o = unit_of<CUT>(p, u + G));
+      if (CUT && now.cols <= 0) continue;
+      const int ch = (now.rg * 2 + (int)rank) * 128 + 32 * q + lane, m0 = now.m0, cols = now.cols;
       epilogue_sync();   // (xs[d] was last read two tiles ago, before the other one's barrier)
       if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
       fence_after_sync();
@@ -684,7 +734,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       });
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[d], 0));
+      // Relaxed: only the reads of tensor memory come before it, and they are done. A release would wait until y is
+      // written (12.2 us become 17.3, 8 rounds of 256 x 32 tokens and four blocks of K).
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&bars.acc_empty[d], 0));
+      ++n;
     }
   }
   fence_before_sync();
@@ -722,6 +775,9 @@ cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<bool>* done) {
   return cudaSuccess;
 }
 
+// Tokens of a piece when the tiles of tn tokens that are left over are cut: each CTA of a pair loads half of them.
+constexpr int cut_tokens(int tn, int cut) { return ((tn + cut - 1) / cut + 31) / 32 * 32; }
+
 // Expected time of a plan in microseconds, in a stream of such calls. The form follows the machine (bytes into
 // an SM, clocks of the tensor core, memory, a start and an end for each tile); the constants are fitted to the
 // times of all plans on 175 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). On 63 other shapes the plan
@@ -733,9 +789,11 @@ double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
   const double memory = ((p.mt > 1 ? 1.35 : 1.0) * N * K + M * K + 2.0 * M * N) / 6.0e6;
   const double tensor = 2.0 * tn / 1900;                           // one block: 8192 products a clock
   if (p.persistent) {
-    const int64_t rounds = (p.tiles + kSMs / 2 - 1) / (kSMs / 2);
-    const double block = std::max(tensor, (16384 + 64.0 * tn) / 101e3);
-    return 3.0 + std::max(rounds * std::max(p.kb * block, 0.024 * tn), memory) + 0.009 * tn;
+    const int64_t rounds = p.tiles / (kSMs / 2), left = p.tiles % (kSMs / 2);
+    auto round = [&](int t) { return std::max(p.kb * std::max(2.0 * t / 1900, (16384 + 64.0 * t) / 101e3), 0.024 * t); };
+    double last = left ? round(tn) : 0;
+    if (p.cut > 1) last = 0.5 + 1.2 * round(cut_tokens(tn, p.cut));
+    return 3.0 + std::max(rounds * round(tn) + last, memory) + 0.009 * tn;
   }
   // two CTAs on their own share an SM; clusters run at once
   const bool alone = p.tiles <= kClusters[cg * p.split];
@@ -753,6 +811,7 @@ double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
   GemmI8Plan o{};
   o.kb = (int)((K + 127) / 128);
+  o.cut = 1;
   double best = 0;
   bool any = false;
   auto offer = [&] {
@@ -778,6 +837,11 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
       if (o.pair) {
         o.persistent = 1;
         offer();
+        // what is left after whole rounds, cut for more pairs
+        const int left = o.tiles % (kSMs / 2);
+        if (o.tiles > kSMs / 2)
+          for (o.cut = 2; left && o.cut <= o.tn / 32 && left * o.cut <= kSMs / 2; ++o.cut) offer();
+        o.cut = 1;
       }
     }
   }
@@ -791,28 +855,36 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   p.tn = pl.tn;
   p.mt = pl.mt;
   p.kb = pl.kb;
-  p.tiles = pl.tiles;
   p.split = pl.split;
+  p.cut = pl.cut;
+  p.cut_tn = cut_tokens(pl.tn, pl.cut);
+  p.whole = pl.cut > 1 ? pl.tiles - pl.tiles % (kSMs / 2) : pl.tiles;
+  p.units = p.whole + (pl.tiles - p.whole) * pl.cut;
   const int stage = 128 * 128 + pl.tn / cg * 128;
   const int cluster = pl.persistent ? 2 : cg * pl.split;
-  const int64_t ctas = (int64_t)(pl.persistent ? std::min(pl.tiles, kSMs / 2) : pl.tiles) * cluster;
+  const int64_t ctas = (int64_t)(pl.persistent ? std::min(p.units, kSMs / 2) : pl.tiles) * cluster;
   // CTAs that have an SM for themselves take the deeper ring
   const int room = cluster > 1 || pl.tiles <= kClusters[1] ? kDeepRing : kRing;
   p.stages = std::min({kMaxStages, room / stage, std::max(1, (pl.kb + pl.split - 1) / pl.split * (pl.persistent ? kMaxStages : 1))});
   p.tmem_cols = 32;
   while (p.tmem_cols < (pl.persistent ? 2 : 1) * pl.tn) p.tmem_cols *= 2;   // two accumulators in the persistent form
   p.err = err;
-  CUtensorMap wmap, xmap;
-  if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg))
+  CUtensorMap wmap, xmap, xmap_cut;
+  if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg) ||
+      (pl.cut > 1 && !encode_bytes_2d(&xmap_cut, a.x, a.K, a.M, a.ldx, p.cut_tn / 2)))
     return cudaErrorInvalidValue;
-  const auto kern = pl.persistent ? gemm_i8_persistent_kernel : pl.pair ? gemm_i8_split_kernel<true> : gemm_i8_split_kernel<false>;
-  static std::atomic<bool> done[3][64];
-  const cudaError_t e = allow_smem(kern, kDeepRing + 1024, done[pl.persistent ? 2 : pl.pair]);
-  if (e != cudaSuccess) return e;
+  static std::atomic<bool> done[4][64];
   // the ring, or the sums that replace it at the end of a split tile
   const int ring = std::max(p.stages * stage, pl.split > 1 ? pl.tn * 512 : 0);
   const int smem = std::max(ring + 1024, (cluster > 1 ? 512 : p.tmem_cols) * kClaimPerColumn);
-  return launch_overlapped(kern, dim3((unsigned)ctas), dim3(kGemmThreads), (size_t)smem, cluster, stream, p, wmap, xmap);
+  auto run = [&](auto kern, int form, auto... maps) {
+    const cudaError_t e = allow_smem(kern, kDeepRing + 1024, done[form]);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(kern, dim3((unsigned)ctas), dim3(kGemmThreads), (size_t)smem, cluster, stream, p, maps...);
+  };
+  if (pl.cut > 1) return run(gemm_i8_persistent_kernel<true>, 3, wmap, xmap, xmap_cut);
+  if (pl.persistent) return run(gemm_i8_persistent_kernel<false>, 2, wmap, xmap, xmap);
+  return pl.pair ? run(gemm_i8_split_kernel<true>, 1, wmap, xmap) : run(gemm_i8_split_kernel<false>, 0, wmap, xmap);
 }
 
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {

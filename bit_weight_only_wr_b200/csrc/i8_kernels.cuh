@@ -69,6 +69,7 @@ struct GemmI8Plan {
   int mt;          // token tiles
   int kb;          // 128-byte blocks of K
   int split;       // parts of a tile's K
+  int cut;         // persistent: pieces of each tile that is left over after whole rounds
   int tiles;
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles

@@ -896,3 +896,12 @@ def test_gemm_i8_where_the_kernel_changes(wr, M, N, K):
     x, w, xs, ws = _i8_case(M, N, K, M + 2 * N + K)
     for ydt in ("f32", "bf16", "f16"):
         _i8_check(wr, x, w, xs, ws, ydt, ldy=N + (M % 2))
+
+
+@pytest.mark.parametrize("M", [250, 256, 289, 505, 512, 1030])
+@pytest.mark.parametrize("N,K", [(19456, 300), (19301, 2560), (9728, 2560), (19200, 130), (22000, 1)])
+def test_gemm_i8_tiles_left_over(wr, M, N, K):
+    """Large products whose tiles come out a few more than whole rounds of the GPU."""
+    x, w, xs, ws = _i8_case(M, N, K, M + 2 * N + K)
+    for ydt in ("f32", "bf16"):
+        _i8_check(wr, x, w, xs, ws, ydt, ldy=N + (M % 2))

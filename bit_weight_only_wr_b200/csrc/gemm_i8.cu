@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 
 // ---- persistent form. Pairs take tiles in turn. With CUT whole rounds only, and each of the tiles that are left over
 // (fewer than pairs) is cut into `cut` pieces of cut_tn tokens for as many pairs: 256 tokens of 19456 x 2560 are 76
-// tiles for 74 pairs, 19.4 us in two rounds and 16.5 with pieces of 32 tokens (512 tokens 24.6 and 22.7).
+// tiles for 74 pairs, 18.9 us in two rounds and 15.5 with pieces of 32 tokens (512 tokens 24.3 and 21.2).
 struct Unit {
   int rg, m0, tn, cols;   // row group, first token, tokens of the MMA, real ones (0 or fewer: nothing to do)
 };
@@ -780,19 +780,18 @@ constexpr int cut_tokens(int tn, int cut) { return ((tn + cut - 1) / cut + 31) /
 
 // Expected time of a plan in microseconds, in a stream of such calls. The form follows the machine (bytes into
 // an SM, clocks of the tensor core, memory, a start and an end for each tile); the constants are fitted to the
-// times of all plans on 175 shapes (M 1 .. 4096, N 64 .. 19456, K 64 .. 16384). On 63 other shapes the plan
-// it picked took 1 %% longer than the best one in the geometric mean, and one CTA a tile with the fewest
-// token tiles and K whole 46 %%.
+// times of all plans on 416 shapes (M 8 .. 4096, N 64 .. 19456, K 64 .. 16384). On 147 other shapes the plan
+// it picked took 2 % longer than the best one in the geometric mean; one CTA a tile with the fewest token tiles
+// and K whole takes 55 % longer.
 double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
   const int cg = 1 + p.pair, tn = p.tn;
   // weights that several token tiles read come from memory more than once now and then
-  const double memory = ((p.mt > 1 ? 1.35 : 1.0) * N * K + M * K + 2.0 * M * N) / 6.0e6;
-  const double tensor = 2.0 * tn / 1900;                           // one block: 8192 products a clock
+  const double memory = ((p.mt > 1 ? 1.23 : 1.0) * N * K + M * K + 2.0 * M * N) / 5.5e6;
+  auto tensor = [](int t) { return 2.0 * t / 1900; };              // one block: 8192 products a clock
   if (p.persistent) {
+    auto round = [&](int t) { return std::max(p.kb * std::max(tensor(t), (16384 + 64.0 * t) / 96.6e3), 0.19 + 0.0153 * t); };
     const int64_t rounds = p.tiles / (kSMs / 2), left = p.tiles % (kSMs / 2);
-    auto round = [&](int t) { return std::max(p.kb * std::max(2.0 * t / 1900, (16384 + 64.0 * t) / 101e3), 0.024 * t); };
-    double last = left ? round(tn) : 0;
-    if (p.cut > 1) last = 0.5 + 1.2 * round(cut_tokens(tn, p.cut));
+    const double last = left == 0 ? 0 : round(p.cut > 1 ? cut_tokens(tn, p.cut) : tn);
     return 3.0 + std::max(rounds * round(tn) + last, memory) + 0.009 * tn;
   }
   // two CTAs on their own share an SM; clusters run at once
@@ -800,9 +799,9 @@ double expected_us(const GemmI8Plan& p, int64_t M, int64_t N, int64_t K) {
   const int64_t waves = alone ? 1 : (p.tiles + 2 * kSMs - 1) / (2 * kSMs), even = (p.tiles + kSMs - 1) / kSMs;
   const int64_t most = alone ? 1 : std::max(2 * waves - 1, std::min(2 * waves, even));   // CTAs of the busiest SM
   const int blocks = (p.kb + p.split - 1) / p.split;
-  const double block = std::max(tensor, (16384 + 128.0 * tn / cg) / 124e3);
-  double t = 0.3 + 0.39 * p.pair + std::max(most * blocks * block, memory) + waves * 2.2;
-  t += p.split > 1 ? 0.64 + 0.014 * cg * cg * p.split * p.split + waves * 0.023 * tn : waves * 0.022 * tn;
+  const double block = std::max(tensor(tn), (16384 + 128.0 * tn / cg) / 123e3);
+  double t = 0.54 + 0.62 * p.pair + std::max(most * blocks * block, memory) + waves * 1.85;
+  t += p.split > 1 ? 0.59 + 0.015 * cg * cg * p.split * p.split + waves * 0.025 * tn : waves * 0.021 * tn;
   return t;
 }
 
@@ -839,8 +838,8 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
         offer();
         // what is left after whole rounds, cut for more pairs
         const int left = o.tiles % (kSMs / 2);
-        if (o.tiles > kSMs / 2)
-          for (o.cut = 2; left && o.cut <= o.tn / 32 && left * o.cut <= kSMs / 2; ++o.cut) offer();
+        if (o.tiles > kSMs / 2 && left)
+          for (o.cut = std::min(o.tn / 32, kSMs / 2 / left); o.cut > 1; --o.cut) offer();
         o.cut = 1;
       }
     }

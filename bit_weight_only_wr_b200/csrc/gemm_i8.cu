@@ -154,7 +154,7 @@ cudaError_t run_gemv(const GemmI8Args& a, cudaStream_t stream) {
 // take turns of 128 bytes of K, U turns at once, and add up in shared memory. The order of K inside an MMA is
 // free as long as both operands keep it: lane 4 g + t loads 32 contiguous bytes of rows g and g + 8 and of
 // tokens g, g + 8, so that rows come in whole 128-byte lines straight into the registers that the MMAs take.
-// 8 tokens of 2560 x 4096 3.8 us (tcgen05 5.2), 4096 x 2560 3.8 (4.9), 6144 x 2560 4.2 (6.2); the last bytes of
+// 8 tokens of 2560 x 4096 3.9 us (tcgen05 5.2), 4096 x 2560 3.3 (4.9), 6144 x 2560 4.0 (6.2); the last bytes of
 // rows stand outside the loop (inside it: 4.5, 2560 x 4096). A ring of bulk copies in its place: 6.3.
 constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
 __device__ __forceinline__ void mma_i8(int c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -891,9 +891,12 @@ cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_few_i8(const GemmI8Args& a, cudaStream_t stream) {
-  // four turns at once where K has them for all warps, else two and a third CTA on the SM (8 tokens of
-  // 2560 x 4096: 3.8 and 4.4 us; of 6144 x 2560: 4.9 and 4.0)
-  const auto kern = a.M > 8 ? few_i8_kernel<2, 2, 2> : a.K >= 4096 ? few_i8_kernel<4, 2, 1> : few_i8_kernel<2, 3, 1>;
+  // Four turns at once and two CTAs an SM, or two turns and a third CTA, by what lets all rows run at once (8
+  // tokens: 4096 x 2560 3.3 and 3.9 us, 4096 x 9728 8.8 and 10.5; 6144 x 2560 5.6 and 4.0). With few of rows
+  // and bytes, and for 2 KB behind 7104 rows, two turns are enough (1024 x 2048: 2.6 and 2.2; 8192 x 2048: 5.6
+  // and 4.9, of 4096 bytes 8.1 and 9.2).
+  const bool deep = a.N <= kFewAtOnce / 3 * 2 ? a.K > 2048 || a.N > 2048 : a.N > kFewAtOnce && a.K > 2048;
+  const auto kern = a.M > 8 ? few_i8_kernel<2, 2, 2> : deep ? few_i8_kernel<4, 2, 1> : few_i8_kernel<2, 3, 1>;
   return launch_overlapped(kern, dim3((unsigned)((a.N + 15) / 16)), dim3(kFewThreads), 0, 1, stream, a);
 }
 

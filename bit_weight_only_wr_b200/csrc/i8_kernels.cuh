@@ -73,14 +73,21 @@ struct GemmI8Plan {
   int tiles;
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
-// The kernel of a call. Measured in a graph of such calls, us (dp4a, warps' MMA, tcgen05):
-//   one token   1024 x 4096: 2.1, 2.6, 4.6;  2560 x 4096: 2.7, 4.0, 5.1;  6144 x 1024: 3.7, 2.6, 3.9
-//   8 tokens    2560 x 4096: -, 3.8, 5.2;    8192 x 4096: -, 8.0, 8.7;    6144 x 9728: -, 15.8, 13.2
+// The kernel of a call. dp4a begins a second turn of rows behind 5328 of them (four in each of nine CTAs an SM),
+// the warps' MMA behind 7104 (sixteen in each of three). Measured in a graph of such calls, us (dp4a, warps' MMA,
+// tcgen05):
+//   one token   2560 x 4096: 2.8, 4.0, 5.1;  6144 x 1024: 3.5, 2.5, 3.9;  6144 x 2560: 4.3, 3.9, -;  6144 x 4096: 5.4, 6.0, -
+//   2 tokens    2560 x 4096: 3.5, 4.0, -;    6144 x 2560: 4.7, 3.9, -;    6144 x 9728: 13.0, 11.5, -
+//   8 tokens    2560 x 4096: -, 4.0, 5.2;    6144 x 9728: -, 11.5, 13.3;  8192 x 4096: -, 8.0, 8.7;  8192 x 5200: -, 12.4, 11.8
 //   16 tokens   4096 x 4096: -, 4.9, 6.6;    6144 x 2560: -, 6.9, 6.0
 enum class I8Kernel { kDp4a, kFew, kTcgen05 };
+constexpr int kFewAtOnce = 148 * 3 * 16;
 inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
-  if (M <= 2 && (K > 1024 || N <= 1024)) return I8Kernel::kDp4a;
-  if (M <= 8 && (N <= 4096 || (N <= 8192 && K <= 4096))) return I8Kernel::kFew;
+  if (M <= 2 && (K > 1024 || N <= 1024)) {
+    const bool second_turn = N > 5328 && N <= kFewAtOnce;
+    return second_turn && (M == 2 || K <= 2560) ? I8Kernel::kFew : I8Kernel::kDp4a;
+  }
+  if (M <= 8 && (N <= kFewAtOnce || (N <= 8192 && K <= 4096))) return I8Kernel::kFew;
   if (M <= 16 && N <= 4096 && K <= 4096) return I8Kernel::kFew;
   return I8Kernel::kTcgen05;
 }

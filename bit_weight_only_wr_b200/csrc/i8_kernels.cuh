@@ -79,7 +79,8 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: t
 //   one token   2560 x 4096: 2.8, 4.0, 5.1;  6144 x 1024: 3.5, 2.5, 3.9;  6144 x 2560: 4.3, 3.9, -;  6144 x 4096: 5.4, 6.0, -
 //   2 tokens    2560 x 4096: 3.5, 4.0, -;    6144 x 2560: 4.7, 3.9, -;    6144 x 9728: 13.0, 11.5, -
 //   8 tokens    2560 x 4096: -, 4.0, 5.2;    6144 x 9728: -, 11.5, 13.3;  8192 x 4096: -, 8.0, 8.7;  8192 x 5200: -, 12.4, 11.8
-//   16 tokens   4096 x 4096: -, 4.9, 6.6;    6144 x 2560: -, 6.9, 6.0
+//   16 tokens   4096 x 4096: -, 5.0, 6.6;    6144 x 2560: -, 6.9, 6.0;    4736 x 6144: -, 7.2, 8.3;  2560 x 9728: -, 8.9, 8.2
+// (9 to 16 tokens have two CTAs an SM: 4736 rows at once).
 enum class I8Kernel { kDp4a, kFew, kTcgen05 };
 constexpr int kFewAtOnce = 148 * 3 * 16;
 inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
@@ -88,7 +89,7 @@ inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
     return second_turn && (M == 2 || K <= 2560) ? I8Kernel::kFew : I8Kernel::kDp4a;
   }
   if (M <= 8 && (N <= kFewAtOnce || (N <= 8192 && K <= 4096))) return I8Kernel::kFew;
-  if (M <= 16 && N <= 4096 && K <= 4096) return I8Kernel::kFew;
+  if (M <= 16 && N <= kFewAtOnce / 3 * 2 && K <= 6144) return I8Kernel::kFew;
   return I8Kernel::kTcgen05;
 }
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);   // M <= 2

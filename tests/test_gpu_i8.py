@@ -907,8 +907,8 @@ def test_gemm_i8_tiles_left_over(wr, M, N, K):
         _i8_check(wr, x, w, xs, ws, ydt, ldy=N + (M % 2))
 
 
-@pytest.mark.parametrize("M", [1, 2, 3, 8])
-@pytest.mark.parametrize("N,K", [(2048, 2048), (2049, 2040), (1030, 2049), (4736, 1500), (4737, 2561), (5328, 2560), (5329, 2560),
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 9, 16])
+@pytest.mark.parametrize("N,K", [(4736, 6144), (4737, 6144), (4736, 6145), (2048, 2048), (2049, 2040), (1030, 2049), (4736, 1500), (4737, 2561), (5328, 2560), (5329, 2560),
                                  (5329, 2561), (7104, 5000), (7105, 2049), (7105, 4097), (7200, 2000)])
 def test_gemm_i8_few_tokens_all_forms(wr, M, N, K):
     """Few tokens on both sides of the sizes that choose among dp4a and the forms of the warps' MMA."""

@@ -915,3 +915,35 @@ def test_gemm_i8_few_tokens_all_forms(wr, M, N, K):
     x, w, xs, ws = _i8_case(M, N, K, M + 2 * N + K)
     for ydt in ("f32", "bf16"):
         _i8_check(wr, x, w, xs, ws, ydt, ldy=N + (M % 2))
+
+
+def test_gemm_i8_tiles_left_over_on_two_streams_and_replayed(wr):
+    """Products whose last tiles are cut, at once on two streams, then replayed from a graph with new tokens."""
+    torch = torch_mod()
+    M, N, K = 256, 19456, 384
+    cases = [_i8_case(M, N, K, seed) for seed in (5, 6)]
+    want = [(x.double() @ w.double().t()).float() * xs[:, None] * ws[None, :] for x, w, xs, ws in cases]
+    ys = [torch.zeros(M, N, device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def call(i):
+        x, w, xs, ws = cases[i]
+        wr.wr_gemm_i8(M, N, K, x, K, xs, w, K, ws, wr.WR_F32, ys[i], N, None, 0, stream=streams[i].cuda_stream)
+
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            call(i)
+    torch.cuda.synchronize()
+    for y, v in zip(ys, want):
+        assert torch.equal(y, v)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        call(0)
+    cases[0][0][:100].zero_()
+    ys[0].fill_(float("nan"))
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not ys[0][:100].any()
+    assert torch.equal(ys[0][100:], want[0][100:])

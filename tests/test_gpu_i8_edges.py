@@ -1,0 +1,70 @@
+"""The 8-bit token path on the GPU where its arithmetic is narrowest: gates of every finite size, the bias in every
+form of the product, rows whose squares are lost one at a time, and calls after a failed one.
+
+Tolerances count roundings; u = 2^-24 is half a step of fp32, relative.
+- silu(g) x: 2^t off by 4 u (2^-22, the approximate instruction), its correction, the sum with 1, the reciprocal
+  (2^-23), and two products: 4 + 1 + 1 + 2 + 1 + 1 = 10 u; the scale's division adds one.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+from gpu_inputs import torch_mod
+from test_gpu_i8 import U, _code, _dt, _gen, _i8_case, _pad16, _quantize, _rows, wr  # noqa: F401  (wr: fixture)
+
+pytestmark = pytest.mark.gpu
+FLT_MAX = float(np.finfo(np.float32).max)
+SILU = 10 * U
+
+
+def _silu64(g):
+    """silu in 64 bits, without an overflow on either side."""
+    torch = torch_mod()
+    e = torch.exp(-g.abs())
+    return torch.where(g >= 0, g / (1 + e), g * e / (1 + e))
+
+
+def _gated_check(wr, gate, x, dt, ld=None):
+    q, s = _quantize(wr, x.to(_dt(dt)), gate=gate.to(_dt(dt)), dt=dt, ld=ld, ldg=ld)
+    torch = torch_mod()
+    v = _silu64(gate.to(_dt(dt)).double()) * x.to(_dt(dt)).double()
+    A = v.abs().amax(1)
+    assert bool(torch.isfinite(s).all())
+    # (scales below 2^-126 round to a step of 2^-149)
+    assert bool(((s.double() - A / 127).abs() <= (SILU + U) * 1.01 * A / 127 + 2.0 ** -149).all()), \
+        float(((s.double() * 127 / A - 1).abs() / U).nan_to_num().max())
+    t = 127 * v / A[:, None]
+    assert float((q.double() - t).abs().max()) <= 0.5 + 127 * (2 * SILU + U)
+
+
+# ---------------------------------------------------------------- gates
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K,ld", [(1, 1), (5, 5), (7, 9), (320, 320), (2560, 2560), (9728, 9729), (40000, 40000)])
+def test_very_large_gates_are_numbers(wr, dt, K, ld):  # noqa: F811
+    """Gates up to the largest finite one: silu(g) = g there, and only a product past fp32 is an infinity."""
+    torch = torch_mod()
+    big = [60.0, 88.0, 89.0, 104.0, 130.0, 1e4, 1e10, 1e30, 2.2e38, 2.4e38, 3e38, 3.38e38]
+    gate = torch.randn(len(big), K, device="cuda", generator=_gen(K))
+    x = torch.randn(len(big), K, device="cuda", generator=_gen(K + 1))
+    gate[:, K // 2] = torch.tensor(big, device="cuda")
+    x[:, K // 2] = torch.where(torch.arange(len(big), device="cuda") % 2 == 0, 0.5, -0.75)
+    _gated_check(wr, gate, x, dt, ld)
+
+
+def test_a_gate_of_the_largest_number_and_infinities(wr):  # noqa: F811
+    torch = torch_mod()
+    gate = torch.full((6, 40), 1.0, device="cuda")
+    x = torch.ones(6, 40, device="cuda")
+    gate[0, 3] = FLT_MAX          # a number
+    gate[1, 3], x[1, 3] = FLT_MAX, 2.0   # the product is not
+    gate[2, 3] = float("inf")
+    gate[3, 3] = float("nan")
+    gate[4, 3], x[4, 3] = -FLT_MAX, FLT_MAX   # silu reads as 0
+    gate[5] = -FLT_MAX
+    q, s = _quantize(wr, x, gate=gate)
+    assert abs(float(s[0]) * 127 / FLT_MAX - 1) <= 12 * U and int(q[0, 3]) == 127 and not q[0, 4:].any()
+    assert bool(torch.isnan(s[1:4]).all()) and not q[1:4].any()
+    assert int(q[4, 3]) == 0 and bool((q[4, 4:] == 127).all())
+    assert float(s[5]) == 0 and not q[5].any()

@@ -307,29 +307,29 @@ __device__ __forceinline__ void store_codes8(int8_t* row, int i, int T, int t, i
   }
 }
 
-// silu(g) x = g x / (1 + 2^(-g log2 e)), off by less than 9 * 2^-24: the exponent t = -g log2 e rounds to
-// t, and what it lost, r, comes back as a first-order term (2^(t + r) = 2^t (1 + r ln 2)); 2^t is off by at
-// most 2^-22.5 and the reciprocal by 2^-23 (the approximate instructions). t is held below 126 so that
-// an overflow cannot meet a zero: there silu is below 1e-36 and reads as 0. g is held below 128 where it enters
-// the exponent, so that t stays finite for every finite g (2^t is 0 there, and silu(g) = g).
+// silu(g) x = g x / (1 + 2^t), t = -g log2 e, off by less than 10 * 2^-24 for every gate from -87.3 on: log2 e has two
+// parts, so that what t loses when it is rounded, and what the first part lacks (1.3e-8 |g| of the result: 19 * 2^-24
+// at g = -86), come back as a first-order term, 2^(t + r) = 2^t (1 + r ln 2). 2^t is off by at most 2^-22 and the
+// reciprocal by 2^-23 (the approximate instructions); the factor, the sum and two products round once each. t is held
+// below 126 so that an overflow cannot meet a zero: there silu is below 1.1e-36 and reads as 0. g is held below 128
+// where it enters the exponent, so that t stays finite for every finite g (2^t is 0 there, and silu(g) = g).
 __device__ __forceinline__ Vec8 silu_mul(const Vec8& g, const Vec8& x) {
-  const f32x2 kLog2e = splat2(-1.4426950408889634f), kLn2 = splat2(0.6931471805599453f), kOne = splat2(1.f);
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;   // log2 e
+  const f32x2 hi2 = splat2(kHi), minus_hi = splat2(-kHi), lo2 = splat2(kLo), minus_ln2 = splat2(-0.6931471805599453f);
+  const f32x2 one = splat2(1.f);
   Vec8 o;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float lo, hi, elo, ehi;
     unpack2(g.p[j], lo, hi);
     const f32x2 held = pack2(fminf(lo, 128.f), fminf(hi, 128.f));
-    f32x2 t = mul2(held, kLog2e);
-    unpack2(t, lo, hi);
+    unpack2(mul2(held, minus_hi), lo, hi);
     lo = fminf(lo, 126.f);
     hi = fminf(hi, 126.f);
-    t = pack2(-lo, -hi);
-    const f32x2 r = fma2(held, kLog2e, t);
+    const f32x2 minus_r = fma2(held, lo2, fma2(held, hi2, pack2(lo, hi)));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(elo) : "f"(lo));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ehi) : "f"(hi));
-    const f32x2 e = pack2(elo, ehi);
-    const f32x2 s = fma2(mul2(e, r), kLn2, add2(e, kOne));
+    const f32x2 s = fma2(pack2(elo, ehi), fma2(minus_r, minus_ln2, one), one);
     unpack2(s, lo, hi);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(elo) : "f"(lo));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ehi) : "f"(hi));

@@ -68,3 +68,21 @@ def test_a_gate_of_the_largest_number_and_infinities(wr):  # noqa: F811
     assert bool(torch.isnan(s[1:4]).all()) and not q[1:4].any()
     assert int(q[4, 3]) == 0 and bool((q[4, 4:] == 127).all())
     assert float(s[5]) == 0 and not q[5].any()
+
+
+@pytest.mark.parametrize("lo,hi", [(-87.3, -80), (-80, -60), (-60, -40), (-40, -20), (-20, -5), (-5, 5), (5, 88), (88, 300)])
+def test_silu_of_one_band_of_gates(wr, lo, hi):  # noqa: F811
+    """Rows of one value, so that each scale shows one silu: within its bound in every band of gates."""
+    torch = torch_mod()
+    M = 60000
+    gate = (lo + (hi - lo) * torch.rand(M, 1, device="cuda", generator=_gen(int(hi)), dtype=torch.float64)).float()
+    x = (1 + torch.rand(M, 1, device="cuda", generator=_gen(3))) * 2.0 ** 60
+    _gated_check(wr, gate, x, "f32")
+
+
+def test_rows_of_negative_gates(wr):  # noqa: F811
+    torch = torch_mod()
+    for at in (-10.0, -40.0, -80.0, -86.0):
+        gate = at + torch.rand(9, 2560, device="cuda", generator=_gen(int(-at)))
+        x = torch.randn(9, 2560, device="cuda", generator=_gen(5)) * 2.0 ** 50
+        _gated_check(wr, gate, x, "f32")

@@ -18,9 +18,13 @@ namespace {
 
 using namespace tc;
 
-__device__ __forceinline__ float scaled(int acc, float xs, float ws, const float* bias, int n) {
-  const float v = (float)acc * xs * ws;
-  return bias ? v + bias[n] : v;
+// The steps from a sum to y, each rounded (the intrinsics are never joined to a multiply-add): every form ends in
+// these two, so that y has the same bits in all of them.
+__device__ __forceinline__ float scaled(int acc, float xs, float ws) { return __fmul_rn(__fmul_rn(__int2float_rn(acc), xs), ws); }
+__device__ __forceinline__ float biased(float v, float bias) { return __fadd_rn(v, bias); }
+__device__ __forceinline__ float finished(int acc, float xs, float ws, const float* bias, int n) {
+  const float v = scaled(acc, xs, ws);
+  return bias ? biased(v, bias[n]) : v;
 }
 __device__ __forceinline__ void store_y(void* y, int type, int64_t at, float v) {
   if (type == WR_F32) static_cast<float*>(y)[at] = v;
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kGemvThreads, 9) gemv_i8_kernel(const GemmI8Ar
       int sum = acc[0];
 #pragma unroll
       for (int m = 1; m < MT; ++m) sum = lane == m ? acc[m] : sum;
-      store_y(a.y, a.y_type, lane * a.ldy + n, scaled(sum, xs, ws, a.bias, n));
+      store_y(a.y, a.y_type, lane * a.ldy + n, finished(sum, xs, ws, a.bias, n));
     }
   }
 }
@@ -250,7 +254,7 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) few_i8_kernel(const GemmI8A
     int sum = 0;
 #pragma unroll
     for (int i = 0; i < kFewWarps; ++i) sum += parts[i][m][threadIdx.x & 15];
-    store_y(a.y, a.y_type, m * a.ldy + n, scaled(sum, a.x_scale[m], ws, a.bias, n));
+    store_y(a.y, a.y_type, m * a.ldy + n, finished(sum, a.x_scale[m], ws, a.bias, n));
   }
 }
 
@@ -366,7 +370,7 @@ __device__ __forceinline__ void store16_half(const GemmI8Args& a, int m, int lef
 __device__ __forceinline__ void store16(const GemmI8Args& a, int m, int left, int ch, int lane, float v[16], float bias) {
   if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] += bias;
+    for (int i = 0; i < 16; ++i) v[i] = biased(v[i], bias);
   }
   if (a.y_type == WR_BF16) return store16_half<Bf16Out>(a, m, left, ch, lane, v);
   if (a.y_type == WR_F16) return store16_half<F16Out>(a, m, left, ch, lane, v);
@@ -387,7 +391,7 @@ __device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16],
                                          float bias) {
   float v[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = (float)sum[i] * xs[i] * ws;
+  for (int i = 0; i < 16; ++i) v[i] = scaled(sum[i], xs[i], ws);
   store16(a, m, left, ch, lane, v, bias);
 }
 
@@ -457,8 +461,8 @@ __device__ __forceinline__ void exchange(const GemmParams& p, const uint8_t* rin
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = (float)sum[i][e] * x * ws[e];
-        if (p.a.bias) v[e] += bias[e];
+        v[e] = scaled(sum[i][e], x, ws[e]);
+        if (p.a.bias) v[e] = biased(v[e], bias[e]);
       }
       const int64_t at = (int64_t)(m0 + tok) * p.a.ldy + ch;
       if (!whole) {

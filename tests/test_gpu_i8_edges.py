@@ -86,3 +86,44 @@ def test_rows_of_negative_gates(wr):  # noqa: F811
         gate = at + torch.rand(9, 2560, device="cuda", generator=_gen(int(-at)))
         x = torch.randn(9, 2560, device="cuda", generator=_gen(5)) * 2.0 ** 50
         _gated_check(wr, gate, x, "f32")
+
+
+# ---------------------------------------------------------------- the product's roundings
+
+SHAPES = [(1, 200, 2000), (2, 513, 4100), (1, 5400, 2560), (3, 640, 2560), (8, 2560, 4096), (12, 4000, 1000), (16, 640, 300),
+          (9, 8192, 640), (17, 300, 128), (64, 256, 4096), (64, 2560, 9728), (40, 6144, 640), (128, 130, 77), (300, 2560, 2560),
+          (333, 2560, 4096), (256, 19456, 640), (512, 9728, 300), (1024, 2560, 512), (2048, 2560, 640)]
+
+
+@pytest.mark.parametrize("ydt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm_i8_rounds_each_step_once(wr, M, N, K, ydt):  # noqa: F811
+    """The conversion, two products and the bias round one after the other, in every form: the bits of the same steps
+    as separate operations."""
+    torch = torch_mod()
+    x, w, xs, ws = _i8_case(M, N, K, M + N + K)
+    bias = torch.randn(N, device="cuda", generator=_gen(N)) * 0.1
+    _, xv = _rows(x, _pad16(K), extra=0)
+    _, wv = _rows(w, _pad16(K), extra=0)
+    acc = (x.double() @ w.double().t()).float()
+    for ld in (N, N + 3):
+        y = torch.empty(M, ld, dtype=_dt(ydt), device="cuda")[:, :N]
+        wr.wr_gemm_i8(M, N, K, xv, _pad16(K), xs, wv, _pad16(K), ws, _code(wr, ydt), y, ld, None, 0, bias=bias)
+        want = acc * xs[:, None]
+        want = want * ws
+        want = want + bias
+        assert torch.equal(y, want.to(_dt(ydt)))
+
+
+def test_gemm_i8_same_bits_for_every_batch_with_a_bias(wr):  # noqa: F811
+    torch = torch_mod()
+    N, K = 2560, 4096
+    x, w, xs, ws = _i8_case(700, N, K, 9)
+    bias = torch.randn(N, device="cuda", generator=_gen(2)) * 0.1
+    rows = []
+    for M in (700, 1, 2, 3, 8, 9, 16, 17, 64, 100, 256, 333):
+        y = torch.empty(M, N, device="cuda")
+        wr.wr_gemm_i8(M, N, K, x, K, xs, w, K, ws, wr.WR_F32, y, N, None, 0, bias=bias)
+        rows.append(y)
+    for y in rows[1:]:
+        assert torch.equal(y, rows[0][:y.shape[0]])

@@ -414,7 +414,7 @@ __device__ __forceinline__ void each16(uint32_t acc, int turn, int cols, F f) {
     for (int b = 0; b < 2; ++b) {
       const int c = c0 + 32 * b;
       if (c >= cols) break;
-      tmem_wait_ld();
+      tmem_wait_ld16(v[b]);
       if (c + 32 < cols) tmem_ld16(acc + c + 32, v[b ^ 1]);
       int sum[16];
 #pragma unroll

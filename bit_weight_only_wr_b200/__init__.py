@@ -23,7 +23,7 @@ __all__ = [
     "wr_quantize_pack", "wr_quantize_trellis", "WR_FMT_T2", "WR_FMT_T8", "wr_quantize_trellis8", "WR_SCALES_I8", "wr_scales_bytes",
     "wr_gemv_batched_plan", "WrGemvGroupItem", "wr_gemv_grouped_workspace_bytes", "wr_gemv_grouped",
     "WR_F32", "WR_BF16", "WR_F16", "WR_I8", "wr_quantize_rows", "wr_gemm_i8_workspace_bytes", "wr_gemm_i8",
-    "WrResidualNormArgs", "wr_residual_norm",
+    "WrResidualNormArgs", "wr_residual_norm", "wr_selftest_gemm_i8_timeout",
 ]
 
 WR_FMT_TERNARY, WR_FMT_Q2, WR_FMT_Q3, WR_FMT_T2, WR_FMT_T8 = 1, 2, 3, 4, 5
@@ -105,6 +105,7 @@ _SIGNATURES = {
     "wr_gemm_i8": (_c_int, [_c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _vp, _vp, _c_int, _vp, _c_i64, _vp,
                             _c_size, _vp]),
     "wr_residual_norm": (_c_int, [ctypes.POINTER(WrResidualNormArgs), _vp]),
+    "wr_selftest_gemm_i8_timeout": (_c_int, [_c_i64, _c_i64, _c_i64, _vp, _c_i64, _vp, _vp, _c_i64, _vp, _vp, _c_i64, _vp]),
 }
 
 
@@ -388,3 +389,9 @@ wr_residual_norm = _marshal.wr_residual_norm
 def wr_selftest_wait_timeout(stream=None) -> None:
     """Launch the failure-path self-test (a bounded wait that runs out after one second)."""
     _check("wr_selftest_wait_timeout", _lib.wr_selftest_wait_timeout(_stream(stream)))
+
+
+def wr_selftest_gemm_i8_timeout(M: int, N: int, K: int, x, ldx: int, x_scale, w, ldw: int, w_scale, y, ldy: int, stream=None) -> None:
+    """Launch a product (fp32 y, no bias) on tcgen05 whose waits give up at once: its failure path. y holds no result."""
+    _check("wr_selftest_gemm_i8_timeout",
+           _lib.wr_selftest_gemm_i8_timeout(M, N, K, _ptr(x), ldx, _ptr(x_scale), _ptr(w), ldw, _ptr(w_scale), _ptr(y), ldy, _stream(stream)))

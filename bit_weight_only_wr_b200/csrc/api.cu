@@ -691,9 +691,9 @@ size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return 0;   // no form needs one: sums that several CTAs share stay in their shared memory
 }
 
-wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
-                     const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,
-                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+static wr_status gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w,
+                         int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y, int64_t ldy, void* stream,
+                         bool short_waits) {
   if (!float_type(y_type)) return WR_ERR_UNSUPPORTED;
   if (check_dims(M, N, K) != WR_OK) return WR_ERR_INVALID_ARG;
   if (K > wr::kMaxI8K) return WR_ERR_UNSUPPORTED;
@@ -703,10 +703,9 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
       !aligned16(y))
     return WR_ERR_INVALID_ARG;
   const wr::I8Kernel kernel = wr::gemm_i8_kernel_for(M, N, K);
+  if (short_waits && kernel != wr::I8Kernel::kTcgen05) return WR_ERR_UNSUPPORTED;
   wr::GemmI8Plan plan{};
   if (kernel == wr::I8Kernel::kTcgen05 && !wr::plan_gemm_i8(M, N, K, &plan)) return WR_ERR_INVALID_ARG;
-  (void)workspace;
-  (void)workspace_bytes;
   wr::GemmI8Args a{};
   a.x = x;
   a.w = w;
@@ -724,8 +723,17 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = kernel == wr::I8Kernel::kDp4a  ? wr::launch_gemv_i8(a, s)
                         : kernel == wr::I8Kernel::kFew ? wr::launch_few_i8(a, s)
-                                                       : wr::launch_gemm_i8(a, plan, device_error_word(), s);
+                                                       : wr::launch_gemm_i8(a, plan, device_error_word(), s,
+                                                                            short_waits ? 0 : wr::kGemmWaitNs);
   return e == cudaSuccess ? WR_OK : WR_ERR_CUDA;
+}
+
+wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
+                     const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,
+                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return gemm_i8(M, N, K, x, ldx, x_scale, w, ldw, w_scale, bias, y_type, y, ldy, stream, false);
 }
 
 wr_status wr_residual_norm(const wr_residual_norm_args* p, void* stream) {
@@ -760,6 +768,11 @@ wr_status wr_selftest_wait_timeout(void* stream) {
   if (wr::launch_selftest_wait_timeout(device_error_word(), static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return WR_ERR_CUDA;
   return WR_OK;
+}
+
+wr_status wr_selftest_gemm_i8_timeout(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
+                                      const int8_t* w, int64_t ldw, const float* w_scale, float* y, int64_t ldy, void* stream) {
+  return gemm_i8(M, N, K, x, ldx, x_scale, w, ldw, w_scale, nullptr, WR_F32, y, ldy, stream, true);
 }
 
 wr_status wr_get_device_error(void* stream) {

@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kFewThreads, CTAS) few_i8_kernel(const GemmI8A
 // epilogue owns one channel and a warp writes 32 neighbouring ones. A tile is 128 channels (256 for a
 // CTA pair) by tn tokens; its K is cut in blocks of 128 bytes, one stage of a ring each (TMA, 128-byte
 // swizzle, zeros behind the ends of K, M and N). Warps: 0 loads (TMA), 1 issues the MMAs, 2-9 are the
-// epilogue (two for each 32 TMEM lanes 32 (warp % 4) .., which take turns of 16 tokens). Every wait is
-// bounded.
+// epilogue (two for each 32 TMEM lanes 32 (warp % 4) .., which take turns of 16 tokens). Every wait on an
+// mbarrier is bounded, and a CTA whose wait ran out still meets the others at every barrier (see settle).
 //
 // CTA pairs (cta_group::2) load each operand once for 256 x tn outputs. Two forms (plan_gemm_i8 chooses
 // by the time it expects of each):
@@ -281,6 +281,7 @@ struct GemmBars {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t copies, mmas, accs;   // how far the roles got: stages filled, stages multiplied, accumulators committed
 };
 
 struct GemmParams {
@@ -288,6 +289,7 @@ struct GemmParams {
   int tn, mt, kb, split, stages, tmem_cols;
   int whole, cut, cut_tn, units;   // persistent form: see unit_of
   int* err;
+  uint64_t wait_ns;   // limit of a wait (0: gives up at its second look)
 };
 
 __device__ __forceinline__ void init_bars(GemmBars& bars, int stages, int empties) {
@@ -301,6 +303,7 @@ __device__ __forceinline__ void init_bars(GemmBars& bars, int stages, int emptie
       mbar_init(&bars.acc_empty[i], empties);
     }
     bars.abort_flag = 0;
+    bars.copies = bars.mmas = bars.accs = 0;
     fence_barrier_init();
   }
 }
@@ -318,12 +321,62 @@ struct Ring {
   }
 };
 
-// On the way out of an aborted CTA: let the copies in flight land (bounded).
-__device__ __forceinline__ void drain(GemmBars& bars, const Ring& r, int stages) {
-  const uint32_t n = min(r.count, (uint32_t)stages);
-  for (uint32_t i = 1; i <= n; ++i) {
-    const uint32_t j = r.count - i;
-    if (!mbar_wait_drain(&bars.full[j % stages], (j / stages) & 1)) break;
+// mbar_wait of a whole warp, which goes on or gives up as one: the lanes decide together. (A vote after every wait in
+// its place: 32 tokens of 6144 x 2560 6.1 -> 6.4 us.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, GemmBars& bars, const GemmParams& p, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  volatile int* abort_flag = &bars.abort_flag;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15u) == 0 || p.wait_ns == 0) {
+      const uint32_t here = __activemask();
+      if (__any_sync(here, *abort_flag != 0)) return false;
+      if (__any_sync(here, global_ns() - t0 >= p.wait_ns)) break;
+    }
+  }
+  *abort_flag = 1;
+  if (p.err) atomicCAS(p.err, 0, code);
+  return false;
+}
+
+// The barrier and parity of the last stage that the loading thread filled. It leaves when that has been multiplied, and
+// with it (commits arrive in order) all of them: no arrival is then under way to this CTA's barriers.
+__device__ __forceinline__ uint64_t* last_empty(GemmBars& bars, const Ring& r, int stages, uint32_t& parity) {
+  parity = r.s == 0 ? r.ph ^ 1 : r.ph;
+  return &bars.empty[r.s == 0 ? stages - 1 : r.s - 1];
+}
+
+// A wait that ran out raises its CTA's flag; before a cluster meets, every warp passes the flag on, so that all of
+// its CTAs leave the same way.
+__device__ __forceinline__ void pass_on_abort(GemmBars& bars, int size, int lane) {
+  __syncwarp();
+  if (*(volatile int*)&bars.abort_flag && lane < size) st_cluster_u32(cluster_addr(&bars.abort_flag, lane), 1);
+}
+
+// On the way out of an aborted cluster, after all of its warps have met: the copies in flight land and the MMAs
+// issued end (bounded waits) before shared and tensor memory are given up. The CTAs of a pair share the leader's
+// `full` barriers and stop independently: what one of them loaded without the other is made up for on the barrier.
+// A CTA loads `bytes` into a stage, cut_bytes from stage cut_from on.
+template <bool PAIR>
+__device__ __noinline__ void settle(GemmBars* bars, uint32_t stages, uint32_t leader, uint32_t bytes, uint32_t cut_bytes,
+                                    uint32_t cut_from) {
+  const bool leads = !PAIR || cluster_rank() == leader;
+  if (threadIdx.x == 0 && leads) {
+    const uint32_t mine = bars->copies, theirs = PAIR ? ld_cluster_u32(cluster_addr(&bars->copies, leader + 1)) : mine;
+    const uint32_t most = max(mine, theirs);
+    for (uint32_t j = most > stages ? most - stages : 0; j < most; ++j) {
+      uint64_t* bar = &bars->full[j % stages];
+      if (j >= mine) mbar_arrive_expect_tx(bar, j >= cut_from ? cut_bytes : bytes);
+      else if (j >= theirs) mbar_complete_tx(bar, j >= cut_from ? cut_bytes : bytes);
+      if (!mbar_wait_drain(bar, (j / stages) & 1)) break;
+    }
+  }
+  if (threadIdx.x == 32) {   // (the commits arrive in both CTAs of a pair)
+    const uint32_t mmas = PAIR ? ld_cluster_u32(cluster_addr(&bars->mmas, leader)) : bars->mmas;
+    const uint32_t accs = PAIR ? ld_cluster_u32(cluster_addr(&bars->accs, leader)) : bars->accs;
+    if (mmas > 0) mbar_wait_drain(&bars->empty[(mmas - 1) % stages], ((mmas - 1) / stages) & 1);
+    if (accs > 0) mbar_wait_drain(&bars->acc_full[(accs - 1) & 1], ((accs - 1) >> 1) & 1);
   }
 }
 
@@ -399,7 +452,16 @@ __device__ __forceinline__ void finish16(const GemmI8Args& a, const int sum[16],
 __device__ __forceinline__ void stage_scales(float* to, const float* x_scale, int cols, int tn, int t) {
   for (int i = t; i < tn; i += kEpilogueThreads) to[i] = i < cols ? x_scale[i] : 0.f;
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueThreads) : "memory"); }
+// The epilogue's threads meet; true if all of them are `ok`, so that after a wait that ran out none goes on without the
+// others.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  int all;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.and.pred q, 1, %2, p;\n selp.s32 %0, 1, 0, q;\n}"
+               : "=r"(all)
+               : "r"((int)ok), "n"(kEpilogueThreads)
+               : "memory");
+  return all != 0;
+}
 
 // This warp's turns of 16 columns of an accumulator, f(first column, sums); the next turn's sums are on
 // their way from tensor memory while f works.
@@ -507,6 +569,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   // A CTA of its own fills the ring before it meets the other warps; a pair's copies complete on the
   // leader's barriers, which have to be there first.
   int k_next = k0;
+  Ring last;   // of the loading thread
   grid_launch_dependents();
   if (warp == 0) {
     if (lane == 0) {
@@ -546,7 +609,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
       bool ok = true;
       for (int k = k0; k < k1; ++k, r.next(p.stages)) {
         if (k < k_next) continue;
-        if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 501))) break;
+        if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 501, p.wait_ns))) break;
         uint8_t* st = ring + r.s * stage_bytes;
         if (PAIR) {
           // both CTAs' copies complete on the leader's barrier
@@ -560,7 +623,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
           tma_load_2d(st + a_bytes, &xmap, k * 128, m0, &bars.full[r.s]);
         }
       }
-      if (!ok && half == 0) drain(bars, r, p.stages);
+      bars.copies = r.count;
+      last = ok ? r : Ring{};
     }
   } else if (warp == 1) {
     if (half == 0) {   // a pair's leader issues for both CTAs
@@ -568,7 +632,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
       Ring r;
       bool ok = true;
       for (int k = k0; k < k1; ++k, r.next(p.stages)) {
-        if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 503))) break;
+        if (!(ok = warp_wait(&bars.full[r.s], r.ph, bars, p, 503))) break;
         fence_after_sync();
         const uint8_t* st = ring + r.s * stage_bytes;
         mma4_i8_ss_commit_elect<PAIR>(tmem, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != k0, &bars.empty[r.s], mask);
@@ -577,9 +641,13 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         if (PAIR) mma_commit_pair_elect(&bars.acc_full[0], mask);
         else mma_commit_elect(&bars.acc_full[0]);
       }
+      if (lane == 0) {
+        bars.mmas = r.count;
+        bars.accs = ok;
+      }
     }
   } else {
-    if (mbar_wait(&bars.acc_full[0], 0, abort_flag, p.err, 504)) {
+    if (warp_wait(&bars.acc_full[0], 0, bars, p, 504)) {
       fence_after_sync();
       const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
       int* mine = reinterpret_cast<int*>(ring) + row;   // [token][channel]; every copy has been consumed
@@ -596,14 +664,25 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
     }
     fence_before_sync();
   }
+  if (size > 1) pass_on_abort(bars, size, lane);
   if (p.split > 1) {
     cluster_sync();   // all parts are in shared memory
     if (!*abort_flag) exchange<CG>(p, ring, xs, part, half, n0, m0, cols, warp, lane);
+  }
+  if (threadIdx.x == 0 && last.count > 0 && !*abort_flag) {   // (here it has arrived; too late to raise the flag)
+    uint32_t parity;
+    uint64_t* bar = last_empty(bars, last, p.stages, parity);
+    mbar_wait_drain(bar, parity);
   }
   fence_before_sync();
   if (size > 1) cluster_sync();   // nobody leaves while its shared memory (or tensor memory) is in use
   else __syncthreads();
   fence_after_sync();
+  if (*abort_flag) {
+    settle<PAIR>(&bars, p.stages, leader, stage_bytes, stage_bytes, 0);
+    if (size > 1) cluster_sync();
+    else __syncthreads();
+  }
   if (warp == 1) {
     if (PAIR) tmem_dealloc_pair(tmem, p.tmem_cols);
     else tmem_dealloc(tmem, p.tmem_cols);
@@ -673,7 +752,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const CUtensorMap* xm = CUT && u >= p.whole ? &xmap_cut : &xmap;
         const uint32_t bytes = a_bytes + (uint32_t)o.tn / 2 * 128;
         for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
-          if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 511))) break;
+          if (!(ok = mbar_wait_bg(&bars.empty[r.s], r.ph ^ 1, abort_flag, p.err, 511, p.wait_ns))) break;
           uint8_t* st = ring + r.s * stage_bytes;
           // both CTAs' copies complete on the leader's barrier
           if (rank == 0) mbar_arrive_expect_tx(&bars.full[r.s], 2 * bytes);
@@ -682,28 +761,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           tma_load_2d_pair(st + a_bytes, xm, k * 128, m0, bar);
         }
       }
-      if (!ok && rank == 0) drain(bars, r, p.stages);
+      bars.copies = r.count;
+      if (ok) {
+        uint32_t parity;
+        uint64_t* bar = last_empty(bars, r, p.stages, parity);
+        mbar_wait_bg(bar, parity, abort_flag, p.err, 515, p.wait_ns);
+      }
     }
   } else if (warp == 1) {
     if (rank == 0) {   // the leader issues for both CTAs
       Ring r;
-      uint32_t n = 0;
+      uint32_t n = 0;   // accumulators committed
       bool ok = true;
       for (int u = worker; ok && u < p.units; u += G) {
         const Unit o = unit_of<CUT>(p, u);
         if (CUT && o.cols <= 0) continue;
         const uint32_t d = n & 1, idesc = idesc_i8s(256, o.tn);
-        if (!(ok = mbar_wait(&bars.acc_empty[d], ((n >> 1) & 1) ^ 1, abort_flag, p.err, 512))) break;
+        if (!(ok = warp_wait(&bars.acc_empty[d], ((n >> 1) & 1) ^ 1, bars, p, 512))) break;
         fence_after_sync();
         for (int k = 0; k < p.kb; ++k, r.next(p.stages)) {
-          if (!(ok = mbar_wait(&bars.full[r.s], r.ph, abort_flag, p.err, 513))) break;
+          if (!(ok = warp_wait(&bars.full[r.s], r.ph, bars, p, 513))) break;
           fence_after_sync();
           const uint8_t* st = ring + r.s * stage_bytes;
           mma4_i8_ss_commit_elect<true>(tmem + d * p.tn, smem_desc_sw128(st), smem_desc_sw128(st + a_bytes), idesc, k != 0,
                                         &bars.empty[r.s], 3);
         }
-        if (ok) mma_commit_pair_elect(&bars.acc_full[d], 3);
+        if (!ok) break;
+        mma_commit_pair_elect(&bars.acc_full[d], 3);
         ++n;
+      }
+      if (lane == 0) {
+        bars.mmas = r.count;
+        bars.accs = n;
       }
     }
   } else {
@@ -729,8 +818,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (u + G < p.units) scales(o = unit_of<CUT>(p, u + G));
       if (CUT && now.cols <= 0) continue;
       const int ch = (now.rg * 2 + (int)rank) * 128 + 32 * q + lane, m0 = now.m0, cols = now.cols;
-      epilogue_sync();   // (xs[d] was last read two tiles ago, before the other one's barrier)
-      if (!mbar_wait(&bars.acc_full[d], (n >> 1) & 1, abort_flag, p.err, 514)) break;
+      // (xs[d] was last read two tiles ago, before the other one's barrier)
+      if (!epilogue_all(warp_wait(&bars.acc_full[d], (n >> 1) & 1, bars, p, 514))) break;
       fence_after_sync();
       const uint32_t acc = tmem + d * p.tn + ((uint32_t)(32 * q) << 16);
       each16(acc, turn, cols, [&](int c0, const int (&sum)[16]) {
@@ -744,9 +833,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       ++n;
     }
   }
+  pass_on_abort(bars, 2, lane);
   fence_before_sync();
   cluster_sync();
   fence_after_sync();
+  if (*abort_flag) {
+    const uint32_t rounds = worker < p.whole ? (p.whole - 1 - worker) / G + 1 : 0;   // whole tiles of this pair
+    settle<true>(&bars, p.stages, 0, stage_bytes, a_bytes + (uint32_t)p.cut_tn / 2 * 128, rounds * p.kb);
+    cluster_sync();
+  }
   if (warp == 1) tmem_dealloc_pair(tmem, p.tmem_cols);
 }
 
@@ -851,7 +946,7 @@ bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p) {
   return true;
 }
 
-cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, cudaStream_t stream) {
+cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, cudaStream_t stream, uint64_t wait_ns) {
   const int cg = 1 + pl.pair;
   GemmParams p{};
   p.a = a;
@@ -872,6 +967,7 @@ cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& pl, int* err, 
   p.tmem_cols = 32;
   while (p.tmem_cols < (pl.persistent ? 2 : 1) * pl.tn) p.tmem_cols *= 2;   // two accumulators in the persistent form
   p.err = err;
+  p.wait_ns = wait_ns;
   CUtensorMap wmap, xmap, xmap_cut;
   if (!encode_bytes_2d(&wmap, a.w, a.K, a.N, a.ldw, 128) || !encode_bytes_2d(&xmap, a.x, a.K, a.M, a.ldx, pl.tn / cg) ||
       (pl.cut > 1 && !encode_bytes_2d(&xmap_cut, a.x, a.K, a.M, a.ldx, p.cut_tn / 2)))

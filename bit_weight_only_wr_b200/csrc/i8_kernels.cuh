@@ -94,7 +94,8 @@ inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
 }
 cudaError_t launch_gemv_i8(const GemmI8Args& a, cudaStream_t stream);   // M <= 2
 cudaError_t launch_few_i8(const GemmI8Args& a, cudaStream_t stream);    // M <= 16
-cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream);
+constexpr uint64_t kGemmWaitNs = 1000000000ull;   // limit of a wait in the tcgen05 forms
+cudaError_t launch_gemm_i8(const GemmI8Args& a, const GemmI8Plan& p, int* err, cudaStream_t stream, uint64_t wait_ns = kGemmWaitNs);
 // Sums of K products of int8 values stay inside int32 up to this K ((-128)^2 * K < 2^31).
 constexpr int64_t kMaxI8K = 131071;
 

@@ -85,13 +85,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 
 // mbar_wait for the background roles (see mbar_try_wait_suspend).
 __device__ __forceinline__ bool mbar_wait_bg(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                             int* err_word, int code) {
+                                             int* err_word, int code, uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait_suspend(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (;;) {
     if (mbar_try_wait_suspend(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (global_ns() - t0 > kWaitLimitNs) break;
+    if (global_ns() - t0 > limit_ns) break;
   }
   *abort_flag = 1;
   if (err_word) atomicCAS(err_word, 0, code);
@@ -310,6 +310,14 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
   asm("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // All threads of the cluster's CTAs (the aligned form: each warp arrives as one).
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -318,6 +326,10 @@ __device__ __forceinline__ void cluster_sync() {
 // Orders nothing but itself: for waits that hand over no memory.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Takes `bytes` that no copy will bring off what a barrier expects.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // tma_load_2d into this CTA's shared memory that completes on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {

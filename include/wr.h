@@ -412,6 +412,13 @@ wr_status wr_get_device_error(void* stream);
  * wr_get_device_error(stream) then returns WR_ERR_TIMEOUT (and clears the word). */
 wr_status wr_selftest_wait_timeout(void* stream);
 
+/* The failure path of wr_gemm_i8's tcgen05 forms: the product (arguments as there; y fp32, no bias) with waits that
+ * give up at once. Where K is long (some ten thousands), a wait runs out in the middle of it, with copies and MMAs in
+ * flight; they end before the kernel returns. y holds no result. WR_ERR_UNSUPPORTED where
+ * wr_gemm_i8 runs on another kernel. Returns WR_OK once launched; wr_get_device_error then as above. */
+wr_status wr_selftest_gemm_i8_timeout(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
+                                      const int8_t* w, int64_t ldw, const float* w_scale, float* y, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

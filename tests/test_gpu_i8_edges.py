@@ -127,3 +127,37 @@ def test_gemm_i8_same_bits_for_every_batch_with_a_bias(wr):  # noqa: F811
         rows.append(y)
     for y in rows[1:]:
         assert torch.equal(y, rows[0][:y.shape[0]])
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("M,N,K", [
+    (40, 20000, 65536),     # a CTA a tile
+    (17, 300, 131071),      # clusters that share a tile
+    (200, 2560, 131071),
+    (300, 2560, 131071),    # clusters of pairs
+    (64, 10240, 65536),     # pairs that take tiles in turn
+    (512, 9728, 65536),     # and cut tiles
+])
+def test_a_product_whose_waits_run_out_ends_and_says_so(wr, M, N, K):  # noqa: F811
+    """The failure path of each tcgen05 form, with copies and MMAs in flight: the kernel ends, the error word tells, and
+    the calls behind it, one of the same form at once among them, are what they should be."""
+    torch = torch_mod()
+    ld = _pad16(K)
+    x = torch.randint(-128, 128, (M, ld), device="cuda", generator=_gen(M), dtype=torch.int8)
+    w = torch.randint(-128, 128, (N, ld), device="cuda", generator=_gen(N), dtype=torch.int8)
+    xs, ws = torch.full((M,), 2.0 ** -20, device="cuda"), torch.ones(N, device="cuda")
+    y, z, lost = (torch.full((M, N), float("nan"), device="cuda") for _ in range(3))
+    assert wr.wr_get_device_error() == 0
+    wr.wr_gemm_i8(M, N, K, x, ld, xs, w, ld, ws, wr.WR_F32, y, N, None, 0)
+    assert wr.wr_get_device_error() == 0
+    for _ in range(3):
+        wr.wr_selftest_gemm_i8_timeout(M, N, K, x, ld, xs, w, ld, ws, lost, N)
+        wr.wr_gemm_i8(M, N, K, x, ld, xs, w, ld, ws, wr.WR_F32, z, N, None, 0)
+        assert wr.wr_get_device_error() == 4
+        assert wr.wr_get_device_error() == 0
+        assert torch.equal(y, z)
+        z.fill_(float("nan"))
+    rows = slice(0, N, max(1, N // 50))
+    ref = (x[:, :K].double() @ w[rows, :K].double().t()) * 2.0 ** -20
+    assert bool(((y[:, rows].double() - ref).abs() <= U * ref.abs()).all())

@@ -776,12 +776,12 @@ wr_status wr_selftest_gemm_i8_timeout(int64_t M, int64_t N, int64_t K, const int
 }
 
 wr_status wr_get_device_error(void* stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return WR_ERR_CUDA;
+  if (wr::own_error(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))) != cudaSuccess) return WR_ERR_CUDA;
   int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return WR_ERR_CUDA;
+  if (wr::own_error(cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int))) != cudaSuccess) return WR_ERR_CUDA;
   if (v != 0) {
     const int zero = 0;
-    if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return WR_ERR_CUDA;
+    if (wr::own_error(cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int))) != cudaSuccess) return WR_ERR_CUDA;
     return WR_ERR_TIMEOUT;
   }
   return WR_OK;

@@ -7,6 +7,12 @@
 
 namespace wr {
 
+// The status of a runtime call, reported here and not again by the next call that asks for the last error.
+inline cudaError_t own_error(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // Launches a product so that it may start while the kernel before it in the stream still runs: its CTAs set up
 // barriers and tensor memory and then wait in grid_dependency_wait() before they touch memory that
 // another kernel may write or read. In a graph of such calls o of one token takes 3.6 us instead of
@@ -29,7 +35,16 @@ inline cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, dim3 bl
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
+  return own_error(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+// A launch in stream order. Its own status is returned, whatever calls before it left behind.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_plain(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  return own_error(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
 // Row quantizer: v = x (or silu(gate) x), one fp32 scale and int8 codes per row.

@@ -548,13 +548,11 @@ template <int VPT, int MAXT, bool VEC>
 cudaError_t run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
   const RowGrid d(a.M, row_threads(a.K, VPT > 0 ? VPT : 4));
   if (a.type == WR_F32) {
-    if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, true, true><<<d.grid, d.block, 0, stream>>>(a);
-    else quantize_rows_kernel<VPT, MAXT, VEC, true, false><<<d.grid, d.block, 0, stream>>>(a);
-  } else {
-    if (a.gate) quantize_rows_kernel<VPT, MAXT, VEC, false, true><<<d.grid, d.block, 0, stream>>>(a);
-    else quantize_rows_kernel<VPT, MAXT, VEC, false, false><<<d.grid, d.block, 0, stream>>>(a);
+    return launch_plain(a.gate ? quantize_rows_kernel<VPT, MAXT, VEC, true, true> : quantize_rows_kernel<VPT, MAXT, VEC, true, false>,
+                        d.grid, d.block, stream, a);
   }
-  return cudaGetLastError();
+  return launch_plain(a.gate ? quantize_rows_kernel<VPT, MAXT, VEC, false, true> : quantize_rows_kernel<VPT, MAXT, VEC, false, false>,
+                      d.grid, d.block, stream, a);
 }
 template <bool VEC>
 cudaError_t run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
@@ -569,9 +567,8 @@ cudaError_t run_quantize(const QuantRowsArgs& a, cudaStream_t stream) {
 template <int VPT, int MAXT, bool VEC, bool B32, bool R32>
 cudaError_t run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {
   const RowGrid d(a.p.M, row_threads(a.p.D, VPT));
-  if (w32) residual_norm_kernel<VPT, MAXT, VEC, B32, R32, true><<<d.grid, d.block, 0, stream>>>(a);
-  else residual_norm_kernel<VPT, MAXT, VEC, B32, R32, false><<<d.grid, d.block, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_plain(w32 ? residual_norm_kernel<VPT, MAXT, VEC, B32, R32, true> : residual_norm_kernel<VPT, MAXT, VEC, B32, R32, false>,
+                      d.grid, d.block, stream, a);
 }
 template <int VPT, int MAXT, bool VEC>
 cudaError_t run_norm(const NormArgs& a, bool w32, cudaStream_t stream) {

@@ -129,6 +129,55 @@ def test_gemm_i8_same_bits_for_every_batch_with_a_bias(wr):  # noqa: F811
         assert torch.equal(y, rows[0][:y.shape[0]])
 
 
+# ---------------------------------------------------------------- after a call that failed
+
+def _driver():
+    lib = ctypes.CDLL("libcuda.so.1")
+    lib.cuStreamBeginCapture_v2.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    lib.cuStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)]
+    return lib
+
+
+def test_a_failed_call_does_not_fail_the_next(wr):  # noqa: F811
+    """A product issued into a capture that has been broken off reports that; the calls after it, on other streams, are
+    not blamed for it."""
+    torch = torch_mod()
+    M, N, K = 40, 64, 256
+    x, w, xs, ws = _i8_case(M, N, K, 1)
+    y, h = torch.zeros(M, N, device="cuda"), torch.randn(M, K, device="cuda", generator=_gen(1))
+    q, s, z = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, K, device="cuda")
+
+    def product(m, stream):
+        wr.wr_gemm_i8(m, N, K, x, K, xs, w, K, ws, wr.WR_F32, y, N, None, 0, stream=stream)
+
+    stream = torch.cuda.Stream()
+    for m in (1, 8, 40):   # each of the product's launches
+        product(m, None)
+    torch.cuda.synchronize()
+    driver = _driver()
+    relaxed = 2
+    for m in (1, 8, 40):
+        assert driver.cuStreamBeginCapture_v2(stream.cuda_stream, relaxed) == 0
+        assert wr.wr_get_device_error(stream) == 3   # a wait for a stream that is being captured: breaks the capture off
+        try:
+            with pytest.raises(wr.WrError) as e:
+                product(m, stream)
+            assert e.value.status == 3
+            wr.wr_quantize_rows(wr.WR_F32, M, K, h, K, q, K, s)
+            wr.wr_residual_norm(M, K, residual=h, ld_residual=K, y=z, ld_y=K)
+            product(m, None)
+        finally:
+            graph = ctypes.c_void_p()
+            assert driver.cuStreamEndCapture(stream.cuda_stream, ctypes.byref(graph)) != 0 and not graph.value
+    # a failure that is not the path's own
+    assert driver.cuStreamBeginCapture_v2(stream.cuda_stream, relaxed) == 0
+    assert wr.wr_get_device_error(stream) == 3
+    driver.cuStreamEndCapture(stream.cuda_stream, ctypes.byref(ctypes.c_void_p()))
+    wr.wr_residual_norm(M, K, residual=h, ld_residual=K, y=z, ld_y=K)
+    torch.cuda.synchronize()
+    assert wr.wr_get_device_error() == 0
+
+
 # ---------------------------------------------------------------- waits that run out
 
 @pytest.mark.parametrize("M,N,K", [

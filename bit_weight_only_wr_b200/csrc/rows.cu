@@ -174,8 +174,11 @@ __device__ __forceinline__ void store8(uint8_t* row, int type, int i, int T, int
 
 // ---------------------------------------------------------------- reductions over a row's CTA
 
-// Every warp leaves its value in buf and every thread reads all of them: one barrier for each
-// reduction (each has its own buf). The sum runs in the same order in every thread and every run.
+// Every warp leaves its value in buf and every warp reduces all of them: one barrier for each
+// reduction (each has its own buf). The sum is a tree, the same in every thread and every run: a row's squares
+// pass through at most 4 VPT + 1 + 5 + 5 roundings. (The warps' sums one after the other: 31 roundings in place of
+// the last 5, 23.8 * 2^-24 off for a row made to show it; 8192 rows of 2560 41.8 us instead of 40.2, 1000 rows of
+// 32768 140 instead of 122.)
 __device__ __forceinline__ float row_sum(f32x2 v2, float* buf) {
   float v, hi;
   unpack2(v2, v, hi);
@@ -186,9 +189,11 @@ __device__ __forceinline__ float row_sum(f32x2 v2, float* buf) {
   if (nw == 1) return v;
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < nw; ++i) s += buf[i];
-  return s;
+  const int lane = threadIdx.x & 31;
+  v = lane < nw ? buf[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 // Largest magnitude, by its bits: an infinity is above every number and a NaN above that.
 __device__ __forceinline__ uint32_t row_max(float amax, uint32_t* buf) {

@@ -129,6 +129,31 @@ def test_gemm_i8_same_bits_for_every_batch_with_a_bias(wr):  # noqa: F811
         assert torch.equal(y, rows[0][:y.shape[0]])
 
 
+# ---------------------------------------------------------------- sums of squares
+
+@pytest.mark.parametrize("D", [2048, 4096, 16384, 32768])
+@pytest.mark.parametrize("M", [1, 400])
+def test_norm_of_a_row_whose_small_squares_come_one_at_a_time(wr, M, D):  # noqa: F811
+    """One value of 1 and, at the start of 256-value stretches, values whose squares are just under half a step of 1:
+    added to the large one after the other all are lost. The sum is a chain of at most 16 squares in a thread and then
+    a tree: 16 + 1 + 5 + 5 roundings, and two of the mean; a root keeps half of these, and adds 4 u of its own (2 ulp);
+    the product after it 1: 19.5 u."""
+    torch = torch_mod()
+    small = float(np.sqrt(np.float64(2.0 ** -24 * 0.98)))
+    for part in (1, 2, 4):
+        h = torch.zeros(M, D, device="cuda")
+        h[:, : D // part : 256] = small
+        for near in (8, 16, 32, 64, 128, *(i * D // part + j for i in range(part) for j in (0, 2, 4, 6))):
+            h[:, near] = small
+        h[:, 0] = 1.0
+        y = torch.empty(M, D, device="cuda")
+        wr.wr_residual_norm(M, D, residual=h, ld_residual=D, y=y, ld_y=D, eps=0.0)
+        v = h.double()
+        ref = v / torch.sqrt((v * v).mean(1, keepdim=True))
+        err = ((y.double() - ref).abs() / ref.abs().clamp_min(1e-30)).max()
+        assert float(err) <= 19.5 * U, float(err) / U
+
+
 # ---------------------------------------------------------------- after a call that failed
 
 def _driver():

@@ -8,6 +8,8 @@ Importing this module fails loudly when the shared library has not been built.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import numpy as np
@@ -115,8 +117,8 @@ def exported_symbols():
 
 
 def _load():
-    if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")):
-        raise ImportError(f"libwr.so or _marshal.so not found beside {LIB_PATH}; build them with "
+    if not os.path.exists(LIB_PATH):
+        raise ImportError(f"libwr.so not found at {LIB_PATH}; build it with "
                           "`python bit_weight_only_wr_b200/build.py` (nvcc, sm_100a)")
     lib = ctypes.CDLL(LIB_PATH)
     for name, (res, args) in _SIGNATURES.items():
@@ -377,13 +379,42 @@ def wr_gemm_i8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 # The calls of the 8-bit token path take about as long on the GPU as ctypes takes to convert their
 # arguments; an extension module does that instead (csrc/python/marshal.cpp; the signatures are in its
-# docstrings). Tensors have to be on the current CUDA device.
-from . import _marshal  # noqa: E402
+# docstrings). Tensors have to be on the current CUDA device. The module is built for one Python version, whose tag its
+# file name carries; without it these three functions say so when they are called, and everything else works.
+MARSHAL_PATH = os.path.join(os.path.dirname(LIB_PATH), "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
-_marshal.set_error(WrError)
-wr_quantize_rows = _marshal.wr_quantize_rows
-wr_gemm_i8 = _marshal.wr_gemm_i8
-wr_residual_norm = _marshal.wr_residual_norm
+
+def _load_marshal():
+    """(module, None), or (None, the reason)."""
+    if not os.path.exists(MARSHAL_PATH):
+        return None, (f"{MARSHAL_PATH} not found; build it with `python bit_weight_only_wr_b200/build.py` "
+                      "(this Python's headers, g++)")
+    try:
+        spec = importlib.util.spec_from_file_location(__name__ + "._marshal", MARSHAL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return None, str(e)
+    module.set_error(WrError)
+    return module, None
+
+
+_marshal, _marshal_missing = _load_marshal()
+
+
+def _marshalled(name):
+    if _marshal is not None:
+        return getattr(_marshal, name)
+
+    def missing(*args, **kwargs):
+        raise ImportError(f"{name}: {_marshal_missing}")
+    missing.__name__ = name
+    return missing
+
+
+wr_quantize_rows = _marshalled("wr_quantize_rows")
+wr_gemm_i8 = _marshalled("wr_gemm_i8")
+wr_residual_norm = _marshalled("wr_residual_norm")
 
 
 def wr_selftest_wait_timeout(stream=None) -> None:

@@ -2,6 +2,7 @@
 Python extension module that marshals arguments for part of it."""
 from __future__ import annotations
 
+import importlib.machinery
 import os
 import subprocess
 import sys
@@ -15,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwr.so")
 MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])   # one file for each Python version
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -66,8 +67,11 @@ def build(verbose: bool = False, extra_nvcc: list[str] | None = None) -> str:
     objs = [os.path.join(BUILD, f + ".o") for f in cu + cpp]
     if jobs or _newer(objs, LIB):
         run([NVCC] + ARCH + ["-shared", "-o", LIB] + objs + ["-Xcompiler", "-fopenmp", "-lgomp"])
-    if _newer([MARSHAL_SRC, LIB, os.path.join(INCLUDE, "wr.h")], MARSHAL):
-        run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+    headers_of_python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers_of_python, "Python.h")):
+        print(f"no Python.h in {headers_of_python}: _marshal is not built, and the 8-bit calls are not to be had from Python")
+    elif _newer([MARSHAL_SRC, LIB, os.path.join(INCLUDE, "wr.h")], MARSHAL):
+        run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-I", headers_of_python,
              MARSHAL_SRC, "-o", MARSHAL, "-L", PKG, "-l:libwr.so", "-Wl,-rpath,$ORIGIN"])
     return LIB
 

@@ -686,10 +686,8 @@ wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_
   return wr::launch_quantize_rows(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? WR_OK : WR_ERR_CUDA;
 }
 
-size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_dims(M, N, K) != WR_OK || K > wr::kMaxI8K) return 0;
-  return 0;   // no form needs one: sums that several CTAs share stay in their shared memory
-}
+// No form needs a workspace: sums that several CTAs share stay in their shared memory.
+size_t wr_gemm_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 static wr_status gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w,
                          int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y, int64_t ldy, void* stream,
@@ -730,9 +728,7 @@ static wr_status gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64
 
 wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t ldx, const float* x_scale,
                      const int8_t* w, int64_t ldw, const float* w_scale, const float* bias, int y_type, void* y,
-                     int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
+                     int64_t ldy, void* /*workspace*/, size_t /*workspace_bytes*/, void* stream) {
   return gemm_i8(M, N, K, x, ldx, x_scale, w, ldw, w_scale, bias, y_type, y, ldy, stream, false);
 }
 

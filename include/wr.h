@@ -361,8 +361,8 @@ wr_status wr_quantize_rows(int type, int64_t M, int64_t K, const void* x, int64_
  * x_scale fp32 [M], w_scale fp32 [N], bias fp32 [N] or null; y of y_type WR_F32, WR_BF16 or WR_F16
  * (ldy >= N). The sums are exact integers; the fp32 conversion, the two products (x_scale first) and
  * the bias round once each, then the type of y does: the result is the same bits on every run and for
- * every M. The workspace rules are those of the other calls; at present no size needs one: the size is 0
- * and the pointer may be null. Up to 16 tokens of matrices that are not too large run on kernels that
+ * every M. No workspace is needed: the size is 0 for all arguments, and the two workspace arguments, kept
+ * for forms that may want one, are not looked at (null and 0 will do). Up to 16 tokens of matrices that are not too large run on kernels that
  * pass over w once by warps, all else on tcgen05 (kind::i8) with the tile, the split of K and the form
  * chosen by the expected time. */
 size_t wr_gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);

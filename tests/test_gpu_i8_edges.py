@@ -235,3 +235,20 @@ def test_a_product_whose_waits_run_out_ends_and_says_so(wr, M, N, K):  # noqa: F
     rows = slice(0, N, max(1, N // 50))
     ref = (x[:, :K].double() @ w[rows, :K].double().t()) * 2.0 ** -20
     assert bool(((y[:, rows].double() - ref).abs() <= U * ref.abs()).all())
+
+
+# ---------------------------------------------------------------- the workspace that is not needed
+
+@pytest.mark.parametrize("M", [1, 8, 16, 40, 300, 1500])
+def test_gemm_i8_with_and_without_a_workspace(wr, M):  # noqa: F811
+    """No size needs a workspace: y is the same without one and with one, which is left as it was."""
+    torch = torch_mod()
+    N, K = 640, 2048
+    x, w, xs, ws = _i8_case(M, N, K, M)
+    space = torch.full((1 << 16,), 7, dtype=torch.uint8, device="cuda")
+    ys = []
+    for workspace, size in ((None, 0), (space, space.numel()), (space.data_ptr() + 8, 4)):
+        y = torch.full((M, N), float("nan"), device="cuda")
+        wr.wr_gemm_i8(M, N, K, x, K, xs, w, K, ws, wr.WR_F32, y, N, workspace, size)
+        ys.append(y)
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2]) and bool((space == 7).all())

@@ -23,6 +23,15 @@ def test_selftest_refusals(change, status):
     assert _status(wr.wr_selftest_gemm_i8_timeout, **{**SELFTEST, **change}) == status
 
 
+def test_gemm_i8_needs_no_workspace():
+    """The size is 0 whatever the arguments, and the workspace arguments are not among those that are checked: calls with
+    none, with one that is not aligned and with a size that is too small are refused (here for ldy) all alike."""
+    for shape in ((1, 64, 64), (40, 70, 9728), (333, 2560, 9728), (4096, 19456, 2560), (16, 1, 131071), (0, 1, 1), (1, 1, 131072)):
+        assert wr.wr_gemm_i8_workspace_bytes(*shape) == 0
+    for workspace, size in ((None, 0), (P + 8, 4), (P, 0), (None, 1 << 40)):
+        assert _status(wr.wr_gemm_i8, **{**GEMM, "ldy": 69, "workspace": workspace, "workspace_bytes": size}) == BAD
+
+
 # ---------------------------------------------------------------- the extension module
 
 def _import_without_module(tmp_path, code, other=None):

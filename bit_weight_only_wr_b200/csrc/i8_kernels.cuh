@@ -89,21 +89,31 @@ struct GemmI8Plan {
 };
 bool plan_gemm_i8(int64_t M, int64_t N, int64_t K, GemmI8Plan* p);   // false: too many tiles
 // The kernel of a call. dp4a begins a second turn of rows behind 5328 of them (four in each of nine CTAs an SM),
-// the warps' MMA behind 7104 (sixteen in each of three). Measured in a graph of such calls, us (dp4a, warps' MMA,
-// tcgen05):
-//   one token   2560 x 4096: 2.8, 4.0, 5.1;  6144 x 1024: 3.5, 2.5, 3.9;  6144 x 2560: 4.3, 3.9, -;  6144 x 4096: 5.4, 6.0, -
-//   2 tokens    2560 x 4096: 3.5, 4.0, -;    6144 x 2560: 4.7, 3.9, -;    6144 x 9728: 13.0, 11.5, -
-//   8 tokens    2560 x 4096: -, 4.0, 5.2;    6144 x 9728: -, 11.5, 13.3;  8192 x 4096: -, 8.0, 8.7;  8192 x 5200: -, 12.4, 11.8
+// the warps' MMA behind 7104 (sixteen in each of three). dp4a's time goes by rows where they are short (0.31 us for a
+// thousand of up to 1536 bytes), and by bytes where they are long. Measured in a graph of such calls, us (dp4a, warps'
+// MMA, tcgen05):
+//   one token   2560 x 4096: 2.9, 4.0, 5.9;  6144 x 1024: 3.5, 2.5, 3.9;  6144 x 2560: 4.3, 3.9, -;  6144 x 4096: 5.4, 6.0, -
+//               8200 x 1024: 4.2, 4.0, 4.6;  16384 x 512: 6.6, 5.0, 4.3;  150000 x 1024: 47, 36, 27;  2560 x 1536: 2.4, 2.8, 4.1
+//               9728 x 1536: 5.0, 4.7, 5.4;  40000 x 1040: 13.7, 14.1, 10.6;  40000 x 1536: 13.8, 12.4, 13.2
+//               150000 x 1536: 48, 38, 37;   9728 x 2560: 5.8, 7.5, 6.9;  150000 x 2560: 57, 70, 59;  19456 x 9728: 32, 38, 31
+//   2 tokens    2560 x 4096: 3.5, 3.9, 6.0;  6144 x 2560: 4.7, 3.9, -;    6144 x 9728: 13.0, 11.5, -;  5328 x 1536: 3.4, 3.1, 5.0
+//               9728 x 1536: 5.7, 4.7, 5.4;  19456 x 2560: 10.8, 11.9, 10.3;  150000 x 2560: 66, 70, 60
+//   8 tokens    2560 x 4096: -, 4.0, 5.2;    6144 x 9728: -, 11.5, 13.3;  8192 x 4096: -, 8.3, 8.7;  8192 x 5200: -, 12.4, 11.1
+//               9728 x 512: -, 3.7, 3.3;     9728 x 1024: -, 4.2, 4.7;    19456 x 1024: -, 6.5, 6.1;  9728 x 2048: -, 5.7, 6.4
+//               40000 x 2048: -, 14.7, 16.8; 150000 x 2048: -, 51, 51;    9728 x 2560: -, 7.4, 7.0;  150000 x 2560: -, 73, 62
+//               19456 x 1536: -, 7.8, 7.5;   150000 x 1536: -, 42, 39
 //   16 tokens   4096 x 4096: -, 5.0, 6.6;    6144 x 2560: -, 6.9, 6.0;    4736 x 6144: -, 7.2, 8.3;  2560 x 9728: -, 8.9, 8.2
-// (9 to 16 tokens have two CTAs an SM: 4736 rows at once).
+//               4752 x 2048: -, 4.8, 5.4
+// (9 to 16 tokens have two CTAs an SM: 4736 rows at once.) On 476 shapes of 1 to 16 tokens and up to 150000 rows the choice
+// takes 1.0 % longer than the best of the three in the geometric mean.
 enum class I8Kernel { kDp4a, kFew, kTcgen05 };
 constexpr int kFewAtOnce = 148 * 3 * 16;
 inline I8Kernel gemm_i8_kernel_for(int64_t M, int64_t N, int64_t K) {
-  if (M <= 2 && (K > 1024 || N <= 1024)) {
+  if (M <= 2 && (K > 2048 || N <= (K > 1024 ? 5328 : 1024))) {
     const bool second_turn = N > 5328 && N <= kFewAtOnce;
     return second_turn && (M == 2 || K <= 2560) ? I8Kernel::kFew : I8Kernel::kDp4a;
   }
-  if (M <= 8 && (N <= kFewAtOnce || (N <= 8192 && K <= 4096))) return I8Kernel::kFew;
+  if (M <= 8 && (N <= kFewAtOnce || (N <= 8192 && K <= 4096) || (K <= 2048 && K >= (N <= 12288 ? 1024 : 1792)))) return I8Kernel::kFew;
   if (M <= 16 && N <= kFewAtOnce / 3 * 2 && K <= 6144) return I8Kernel::kFew;
   return I8Kernel::kTcgen05;
 }

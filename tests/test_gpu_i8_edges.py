@@ -95,8 +95,14 @@ SHAPES = [(1, 200, 2000), (2, 513, 4100), (1, 5400, 2560), (3, 640, 2560), (8, 2
           (333, 2560, 4096), (256, 19456, 640), (512, 9728, 300), (1024, 2560, 512), (2048, 2560, 640)]
 
 
+# both sides of where short rows go from one kernel to another
+SHORT_ROWS = [(m, n, k) for m in (1, 2) for n, k in ((1024, 1024), (1025, 1024), (1030, 1025), (5328, 1025), (5329, 1025), (5328, 2048), (5329, 2048),
+                                                   (5329, 2049), (8193, 1023), (8193, 1024), (12288, 1025), (12289, 1025), (12289, 1791), (12289, 1792), (12289, 2049), (20000, 1100))]
+SHORT_ROWS += [(m, n, k) for m in (3, 8, 9) for n, k in ((8193, 1023), (8193, 1024), (12288, 2048), (12289, 1791), (12289, 1792), (12301, 2049), (8193, 4096))]
+
+
 @pytest.mark.parametrize("ydt", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + SHORT_ROWS)
 def test_gemm_i8_rounds_each_step_once(wr, M, N, K, ydt):  # noqa: F811
     """The conversion, two products and the bias round one after the other, in every form: the bits of the same steps
     as separate operations."""

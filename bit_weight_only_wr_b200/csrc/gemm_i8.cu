@@ -74,8 +74,9 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc) {
 // `share` warps (1, 2 or 4) of a CTA share a row of w and read it once, 512 bytes a warp and step with eight
 // steps in flight; x comes from L1. Memory latency is what a matrix of this size is bound by, so share is
 // what lets a warp have all of its bytes on their way at once (up to K = 16384). Where there are rows for more
-// than two rounds of CTAs, a CTA takes rows in turn (19456 rows of 2560: 9.2 us, a CTA for every four rows
-// 10.0; 6144 rows: 4.6 and 4.3).
+// than two rounds of CTAs, a CTA takes rows in turn: 21312 rows of 2064 bytes 8.8 us, a CTA for every four rows 9.7;
+// 40000 of 2560 with two tokens 18.8 and 19.9, with one 17.2 and 17.0; of 9728 66 and 64. In two rounds and fewer the
+// two differ either way (7992 rows of 4096: 7.3 and 6.7, 10656 rows of 2560: 5.6 and 6.1).
 constexpr int kGemvThreads = 128, kGemvCtas = 148 * 9;   // nine CTAs fill an SM's registers
 template <int MT>
 __global__ void __launch_bounds__(kGemvThreads, 9) gemv_i8_kernel(const GemmI8Args a, const int share) {

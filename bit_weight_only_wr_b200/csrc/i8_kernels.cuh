@@ -15,9 +15,9 @@ inline cudaError_t own_error(cudaError_t e) {
 
 // Launches a product so that it may start while the kernel before it in the stream still runs: its CTAs set up
 // barriers and tensor memory and then wait in grid_dependency_wait() before they touch memory that
-// another kernel may write or read. In a graph of such calls o of one token takes 3.6 us instead of
-// 3.9, q/k/v of 32 tokens 7.1 instead of 7.6, down of 333 tokens 13.4 instead of 14.6; norm and q/k/v of
-// 32 tokens together 10.6 instead of 11.4. (The row operators are launched plainly: their many small
+// another kernel may write or read. In a graph of such calls o of one token takes 2.9 us instead of
+// 3.7, q/k/v of 32 tokens 6.2 instead of 7.5, down of 333 tokens 13.8 instead of 14.7; norm and q/k/v of
+// 32 tokens together 9.0 instead of 10.6. (The row operators are launched plainly: their many small
 // CTAs, started early, took slots from the kernel before; 8192 rows 45 instead of 40 us.)
 template <typename... Params, typename... Args>
 inline cudaError_t launch_overlapped(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream,
@@ -62,7 +62,7 @@ cudaError_t launch_quantize_rows(const QuantRowsArgs& a, cudaStream_t stream);
 
 // Residual + norm around a block (wr_residual_norm_args, checked).
 cudaError_t launch_residual_norm(const wr_residual_norm_args& a, cudaStream_t stream);
-constexpr int64_t kMaxNormDim = 32768;   // a row's values stay in the registers of one CTA
+constexpr int64_t kMaxNormDim = 32768;   // a row stays in one CTA
 
 // Int8 product.
 struct GemmI8Args {

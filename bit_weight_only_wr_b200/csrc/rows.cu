@@ -7,7 +7,10 @@
 //
 // Both are bound by memory: every input is read once and every output written once. One CTA owns a
 // row and keeps its values in registers between the reductions, so that nothing is read twice; a
-// thread holds VPT vectors of 8 elements. All arithmetic is fp32 and rounds once to the output's type.
+// thread holds VPT vectors of 8 elements. Not all of a norm's fit where a row is longer than 16384: four
+// vectors of each operand in 64 registers (1024 threads) leave 0.25 to 1.4 KB a thread in local memory, and
+// 1000 bf16 rows of 20000 take 82 us and of 32768 121, of 16384 43. Quantizer rows of more than 32768 are read
+// twice: 1000 bf16 rows of 50000 take 71 us, gated 110; of 32768 gated 44. All arithmetic is fp32 and rounds once to the output's type.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -527,12 +530,12 @@ inline bool rows_aligned(int64_t M, int64_t ld, int bytes) { return M == 1 || ld
 inline int row_threads(int64_t D, int vpt) { return (int)std::min<int64_t>(1024, ((D + 8 * vpt - 1) / (8 * vpt) + 31) / 32 * 32); }
 
 // Vectors a thread. Few rows: one or two, the shortest way through a row (one gated row of 9728 fp32 values:
-// 3.2 us with two, 3.9 with four). Many: two, since a thread's work in the
+// 3.5 us with two, 3.9 with four). Many: two, since a thread's work in the
 // reductions is the same for 16 elements as for 8 and instructions run out before bandwidth does, while
-// four leave too few warps to hide the loads (8192 rows of 2560, fp32 block, bf16 residual: 48.0, 37.5 and
-// 58.8 us with one, two and four; 500 rows: 5.0, 4.6 and 6.6). Four where two would make a CTA of more
+// four leave too few warps to hide the loads (8192 rows of 2560, fp32 block, bf16 residual, a gate: 46.6, 40.5
+// and 58.7 us with one, two and four; 500 rows: 5.1, 5.2 and 6.4). Four where two would make a CTA of more
 // than `most` threads: the quantizer holds less and gains from four earlier (2000 gated rows of 8192 bf16:
-// 15.4 against 18.8 us; the norm: 37.6 against 31.9).
+// 19.0 against 22.2 us; the norm: 39.7 against 33.2).
 constexpr int64_t kManyRows = 2 * 148;
 inline int row_vpt(int64_t M, int64_t D, int most) {
   const int64_t vecs = (D + 7) / 8;

@@ -382,8 +382,8 @@ wr_status wr_gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t* x, int64_t l
  * or residual, and residual_out or y, have to be there. residual_out may be residual (with the same
  * stride); other outputs overlap no input. ld_gate = 0: one gate vector for all rows. Types: block,
  * residual (and residual_out), gate and weights each WR_F32, WR_BF16 or WR_F16 (0 where unused).
- * 1 <= D <= 32768 (larger D: WR_ERR_UNSUPPORTED); eps >= 0, all three floats finite. A row of zeros
- * needs eps > 0 to stay zero (0 / 0 otherwise). Squares are summed in fp32, of scaled values where the sum
+ * 1 <= D <= 32768 (larger D: WR_ERR_UNSUPPORTED; beyond 16384 an element takes about 1.5 times as long);
+ * eps >= 0, all three floats finite. A row of zeros needs eps > 0 to stay zero (0 / 0 otherwise). Squares are summed in fp32, of scaled values where the sum
  * would leave its range (a row of subnormal numbers with eps = 0 has no finite reciprocal all the same). */
 typedef struct {
   int64_t M, D;

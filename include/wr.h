@@ -343,7 +343,7 @@ enum { WR_F32 = 0, WR_BF16 = 1, WR_F16 = 2, WR_I8 = 3 };
 /* Row quantizer (device): for each of M rows of K values v = x[m,k], or v = silu(gate[m,k]) * x[m,k]
  * in fp32 where gate is not null (the input of an MLP's down projection from its gate and up products,
  * which may be two halves of one buffer), with silu(g) = g / (1 + exp(-g)), v off by less than 10 * 2^-24 of
- * its size (silu of a gate below -87.3, less than 1.1e-36 in magnitude, reads as 0):
+ * its size where it is a normal number (silu of a gate below -87.3, less than 1.1e-36 in magnitude, reads as 0):
  *     scale[m] = A / 127,  A = max_k |v|        (fp32)
  *     q[m,k]   = the integer nearest to 127 v / A, a tie to the even one
  * so that v is about q * scale. The choice of q is exact for the fp32 value v (decided on the exact

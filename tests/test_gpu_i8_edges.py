@@ -55,19 +55,21 @@ def test_very_large_gates_are_numbers(wr, dt, K, ld):  # noqa: F811
 
 def test_a_gate_of_the_largest_number_and_infinities(wr):  # noqa: F811
     torch = torch_mod()
-    gate = torch.full((6, 40), 1.0, device="cuda")
-    x = torch.ones(6, 40, device="cuda")
+    gate = torch.full((7, 40), 1.0, device="cuda")
+    x = torch.ones(7, 40, device="cuda")
     gate[0, 3] = FLT_MAX          # a number
     gate[1, 3], x[1, 3] = FLT_MAX, 2.0   # the product is not
     gate[2, 3] = float("inf")
     gate[3, 3] = float("nan")
     gate[4, 3], x[4, 3] = -FLT_MAX, FLT_MAX   # silu reads as 0
     gate[5] = -FLT_MAX
+    gate[6, 3] = -float("inf")    # -inf / inf
     q, s = _quantize(wr, x, gate=gate)
     assert abs(float(s[0]) * 127 / FLT_MAX - 1) <= 12 * U and int(q[0, 3]) == 127 and not q[0, 4:].any()
     assert bool(torch.isnan(s[1:4]).all()) and not q[1:4].any()
     assert int(q[4, 3]) == 0 and bool((q[4, 4:] == 127).all())
     assert float(s[5]) == 0 and not q[5].any()
+    assert bool(torch.isnan(s[6])) and not q[6].any()
 
 
 @pytest.mark.parametrize("lo,hi", [(-87.3, -80), (-80, -60), (-60, -40), (-40, -20), (-20, -5), (-5, 5), (5, 88), (88, 300)])
